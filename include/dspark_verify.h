@@ -77,7 +77,9 @@ typedef enum {
   DSPARK_ERR_WORKSPACE = 4
 } dspark_status_t;
 
-typedef enum { DSPARK_BF16 = 0, DSPARK_F32 = 1 } dspark_dtype_t;
+/* DSPARK_F16 is a type of the cache-side calls (dspark_attention.h); the verify calls take
+ * DSPARK_BF16 and DSPARK_F32 logits. */
+typedef enum { DSPARK_BF16 = 0, DSPARK_F32 = 1, DSPARK_F16 = 2 } dspark_dtype_t;
 
 /* Per-sequence bits written to out.status[b]. */
 #define DSPARK_SEQ_BAD_DRAFT 1     /* a draft id outside [0, V)                           */

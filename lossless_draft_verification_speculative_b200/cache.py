@@ -1,0 +1,268 @@
+"""Python binding of ``include/dspark_attention.h``: the cache side of a verify cycle.
+
+``rotary_append`` rotates each sequence's new tokens and appends their keys and values to the
+paged cache; ``block_attention`` attends them over it; ``rotary_frequencies`` makes the
+rotary frequencies. As in ``binding.py`` the work runs in the CUDA library: this module checks
+layouts, allocates results and workspace with PyTorch, and passes pointers and the current
+stream of the tensors' device. The calls are not differentiable.
+
+Rows come in one of two forms: a block ``[B, N, heads, head_dim]`` of which sequence b uses its
+first ``n_new[b]`` rows (all N without ``n_new``), the form of ``mixed_accept``'s batch; or
+packed rows ``[T, heads, head_dim]`` with ``q_start`` (int32 ``[B+1]``), sequence b's rows being
+``q_start[b]`` to ``q_start[b+1] - 1``. Other rows are left as they were.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Tuple, Union
+
+import torch
+
+from .binding import DSPARK_OK, DsparkError, load_library
+
+SEQ_BAD_PAGE = 32
+CACHE_DTYPES = {torch.bfloat16: 0, torch.float16: 2}
+ROTARY_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+# turns in the trained context that bound the ramp of each scaling, where the caller names none
+_RAMP = {"yarn": (1.0, 32.0), "bands": (1.0, 4.0)}
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("seq_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("n_new", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_page_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+                ("max_pages", ctypes.c_int), ("kv_len", ctypes.c_void_p)]
+
+
+def _lib() -> ctypes.CDLL:
+    lib = load_library()
+    if getattr(lib, "_cache_side", False):
+        return lib
+    vp, i32, sz, f32, f64 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float,
+                             ctypes.c_double)
+    lib.dspark_rotary_frequencies.restype = i32
+    lib.dspark_rotary_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp, vp]
+    lib.dspark_rotary_append.restype = i32
+    lib.dspark_rotary_append.argtypes = [Heads, i32, Heads, Heads, Heads, i32, KvCache, Rows, vp,
+                                         i32, i32, f32, vp, vp]
+    lib.dspark_block_attention_workspace_bytes.restype = sz
+    lib.dspark_block_attention_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.dspark_block_attention.restype = i32
+    lib.dspark_block_attention.argtypes = [Heads, i32, Heads, i32, KvCache, Rows, f32, i32, i32,
+                                           vp, vp, vp, sz, vp]
+    lib._cache_side = True
+    return lib
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _int32(t: torch.Tensor, n: int, name: str, device) -> None:
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != device or \
+            (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on q's device")
+
+
+def _check_rows(q: torch.Tensor, kv_len: torch.Tensor, n_new: Optional[torch.Tensor],
+                q_start: Optional[torch.Tensor]) -> Rows:
+    if not q.is_cuda:
+        raise RuntimeError("the cache-side calls run on CUDA tensors only")
+    if q.dtype not in CACHE_DTYPES:
+        raise ValueError("q must be bfloat16 or float16")
+    B = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    _int32(kv_len, B, "kv_len", q.device)
+    if q_start is not None:
+        if n_new is not None:
+            raise ValueError("n_new belongs to a block of rows, q_start to packed ones")
+        if q.dim() != 3:
+            raise ValueError("with q_start, q must be [T, heads, head_dim]")
+        _int32(q_start, B + 1, "q_start", q.device)
+        return Rows(B, q.shape[0], None, q_start.data_ptr())
+    if q.dim() != 4 or q.shape[0] != B:
+        raise ValueError("q must be [B, N, heads, head_dim] (or packed, with q_start)")
+    if n_new is not None:
+        _int32(n_new, B, "n_new", q.device)
+    return Rows(B, q.shape[1], _ptr(n_new), None)
+
+
+def _heads(t: torch.Tensor, like: torch.Tensor, heads: int, name: str) -> Heads:
+    """The head-row tensor t: the rows and element type of `like`, `heads` heads."""
+    if t.dtype != like.dtype or t.device != like.device or t.dim() != like.dim() or \
+            t.shape[:-2] != like.shape[:-2] or t.shape[-2] != heads or \
+            t.shape[-1] != like.shape[-1] or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have {heads} heads of q's rows, head_dim, dtype and "
+                         "device, its last dimension contiguous")
+    s = t.stride()
+    return Heads(t.data_ptr(), s[0] if len(s) == 4 else 0, s[-3], s[-2])
+
+
+def _check_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                 kv_len: torch.Tensor, q: torch.Tensor) -> KvCache:
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != q.shape[-1]:
+        raise ValueError("k_pages and v_pages must be [pages, page_size, heads, head_dim] with "
+                         "q's head_dim")
+    if k_pages.dtype != q.dtype or v_pages.dtype != q.dtype or k_pages.device != q.device or \
+            v_pages.device != q.device:
+        raise ValueError("k_pages and v_pages must have q's dtype and device")
+    ks, vs = k_pages.stride(), v_pages.stride()
+    if k_pages.shape[3] > 1 and (ks[3] != 1 or vs[3] != 1):
+        raise ValueError("the last dimension of the pages must be contiguous")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+            page_table.shape[0] != kv_len.shape[0] or page_table.device != q.device or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be an int32 [B, max_pages] tensor on q's device with "
+                         "contiguous rows")
+    n_pages, ps, heads, D = k_pages.shape
+    cols = page_table.shape[1]
+    # (a table of one row has no row stride to speak of)
+    ld = page_table.stride(0) if page_table.shape[0] > 1 else cols
+    return KvCache(k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1],
+                   vs[2], n_pages, ps, heads, D, page_table.data_ptr(), ld, cols,
+                   kv_len.data_ptr())
+
+
+def _run(device, fn, what: str, *args) -> None:
+    """Call the library on the tensors' device and its current stream."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != DSPARK_OK:
+        raise DsparkError(rc, what)
+
+
+def rotary_frequencies(rotary_dim: int, theta: float = 10000.0, *,
+                       scaling: Optional[str] = None, factor: float = 1.0,
+                       trained: float = 8192.0, low: Optional[float] = None,
+                       high: Optional[float] = None) -> Tuple[torch.Tensor, float]:
+    """The rotary frequencies (float32 ``[rotary_dim / 2]`` on the CPU) and the magnitude that
+    ``rotary_append`` takes.
+
+    ``scaling`` stretches them for contexts ``factor`` times the ``trained`` one: ``"linear"``
+    (every frequency divided), ``"ntk"`` (a larger base), ``"yarn"`` (a ramp over the number of
+    turns in the trained context, with a magnitude) or ``"bands"`` (low frequencies divided,
+    high ones kept, a smooth band between). ``low`` and ``high`` bound the ramp in turns
+    (1 and 32 for yarn, 1 and 4 for bands).
+    """
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError("scaling must be None, 'linear', 'ntk', 'yarn' or 'bands'")
+    lo, hi = _RAMP.get(scaling, (1.0, 4.0))
+    freq = torch.empty(max(1, int(rotary_dim) // 2), dtype=torch.float32)
+    mag = ctypes.c_float(1.0)
+    rc = _lib().dspark_rotary_frequencies(
+        int(rotary_dim), float(theta), ROTARY_SCALINGS[scaling], float(factor), float(trained),
+        lo if low is None else float(low), hi if high is None else float(high),
+        freq.data_ptr(), ctypes.addressof(mag))
+    if rc != DSPARK_OK:
+        raise DsparkError(rc, "dspark_rotary_frequencies")
+    return freq, float(mag.value)
+
+
+def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
+                  v_pages: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                  inv_freq: Optional[torch.Tensor], *, n_new: Optional[torch.Tensor] = None,
+                  q_start: Optional[torch.Tensor] = None, interleaved: bool = False,
+                  magnitude: float = 1.0, out: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotate the new tokens' queries and keys and append keys and values to the paged cache.
+
+    ``q`` has the rows of a block or packed rows (see the module), ``k`` and ``v`` the same rows
+    with the cache's heads. ``k_pages`` and ``v_pages`` are ``[pages, page_size, heads,
+    head_dim]`` (any strides with contiguous head_dim); new token i of sequence b goes to
+    position ``kv_len[b] - n + i`` through ``page_table`` (int32 ``[B, max_pages]``): ``kv_len``
+    (int32 ``[B]``) counts the new tokens. ``inv_freq`` (float32, on the device) rotates the
+    first ``2 len(inv_freq)`` elements of each head, as halves or as ``interleaved`` pairs; None
+    rotates nothing. Returns the rotated queries (``out``, which may be ``q``). ``status`` (int32
+    ``[B]``) receives SEQ_BAD_PARAM / SEQ_BAD_PAGE bits.
+    """
+    lib = _lib()
+    rows = _check_rows(q, kv_len, n_new, q_start)
+    cache = _check_cache(k_pages, v_pages, page_table, kv_len, q)
+    dev = q.device
+    R = 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.device != dev or \
+                not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous float32 vector on q's device")
+        R = 2 * inv_freq.shape[0]
+        if R > q.shape[-1]:
+            raise ValueError("inv_freq rotates more elements than a head has")
+    if status is not None:
+        _int32(status, rows.B, "status", dev)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    Hq, Hk = q.shape[-2], k_pages.shape[2]
+    _run(dev, lib.dspark_rotary_append, "dspark_rotary_append", _heads(q, q, Hq, "q"), Hq,
+         _heads(out, q, Hq, "out"), _heads(k, q, Hk, "k"), _heads(v, q, Hk, "v"),
+         CACHE_DTYPES[q.dtype], cache, rows, _ptr(inv_freq), R, int(interleaved),
+         float(magnitude), _ptr(status))
+    return out
+
+
+def block_attention_workspace_bytes(N: int, n_q_heads: int, n_heads: int, head_dim: int) -> int:
+    return int(_lib().dspark_block_attention_workspace_bytes(N, n_q_heads, n_heads, head_dim))
+
+
+def block_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                    page_table: torch.Tensor, kv_len: torch.Tensor, *,
+                    n_new: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
+                    scale: Optional[float] = None, causal: bool = True,
+                    window: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of the new tokens over the paged cache, which already holds their keys.
+
+    ``q`` (a block or packed rows, see the module) is already rotated; query head h reads cache
+    head ``h // (heads of q / heads of the cache)``. New token i of sequence b sits at position
+    ``p = kv_len[b] - n + i`` and sees the positions below ``kv_len[b]`` that are ``<= p`` when
+    ``causal`` (not: the whole block, as a block drafter does) and ``> p - window`` when a
+    ``window`` is given. ``scale`` defaults to ``head_dim ** -0.5``. Returns ``out``, q's shape;
+    a token that sees nothing gives zeros. ``lse`` (float32, q's shape without head_dim)
+    receives the logarithm of each row's sum of exponentials, ``status`` (int32 ``[B]``) the
+    SEQ_* bits. ``workspace``: at least ``block_attention_workspace_bytes(N, ...)`` bytes; by
+    default one is taken from PyTorch's allocator for each call.
+    """
+    lib = _lib()
+    rows = _check_rows(q, kv_len, n_new, q_start)
+    cache = _check_cache(k_pages, v_pages, page_table, kv_len, q)
+    dev = q.device
+    Hq, Hk, D = q.shape[-2], k_pages.shape[2], q.shape[-1]
+    if window is not None and window < 1:
+        raise ValueError("window must be at least 1 (None: no window)")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:-1] or
+                            lse.device != dev or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor of q's shape without head_dim")
+    if status is not None:
+        _int32(status, rows.B, "status", dev)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if workspace is None:
+        nbytes = lib.dspark_block_attention_workspace_bytes(rows.N, Hq, Hk, D)
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    _run(dev, lib.dspark_block_attention, "dspark_block_attention", _heads(q, q, Hq, "q"), Hq,
+         _heads(out, q, Hq, "out"), CACHE_DTYPES[q.dtype], cache, rows,
+         1.0 / math.sqrt(D) if scale is None else float(scale), int(causal),
+         0 if window is None else min(int(window), 0x7fffffff), _ptr(lse), _ptr(status), workspace.data_ptr(),
+         workspace.numel() * workspace.element_size())
+    return out

@@ -7,17 +7,19 @@
 #include <cstring>
 #include <mutex>
 
+#include "attention.cuh"
 #include "common.cuh"
 #include "early_exit.cuh"
 #include "finish.cuh"
 #include "markov.cuh"
 #include "markov_mma.cuh"
+#include "rotary.cuh"
 #include "stream.cuh"
 
 namespace dspark {
 namespace {
 
-constexpr int kAbiVersion = 6;  // 6: dspark_pipeline_timeouts
+constexpr int kAbiVersion = 7;  // 7: dspark_attention.h
 constexpr int kMaxDevices = 64;
 
 // Tuning switch, read at every call: DSPARK_MAX_CTAS caps the pass-1 CTAs (0 = one per SM).
@@ -966,3 +968,5 @@ dspark_status_t dspark_speculative_sample_accept_static(const void* p1, int64_t 
 }
 
 }  // extern "C"
+
+#include "attention_abi.cuh"  // dspark_attention.h, with the launch helpers above
