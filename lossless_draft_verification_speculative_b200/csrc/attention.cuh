@@ -1,9 +1,60 @@
-// Attention of a call's new tokens over the paged cache (dspark_block_attention).
+// Attention of a call's new tokens over the paged cache (dspark_block_attention), on the
+// fifth-generation tensor cores (tcgen05).
+//
+// Mathematics. For one new token and query head, out = sum_t e^(z_t) v_t / sum_t e^(z_t),
+// z_t = scale q . k_t over the seen positions t. One pass over the keys with the running
+// maximum m and sum l of the softmax: a tile of 128 positions adds p_t = 2^(c z_t - c m) to l and
+// p_t v_t to O (c = log2 e); when a new maximum exceeds m by more than 8 binary orders, l and O
+// are scaled by 2^(c m - c m'). Smaller excesses leave m as it is: p then reaches at most 2^8,
+// which costs float32 and the 16-bit weights no precision, and the rescaling of O is rare.
+//
+// What bounds it. The keys and values of a cache head are read once for all G query heads that
+// share it and all new tokens of the sequence: with few tokens 2 head_dim 2 bytes of HBM per
+// position are the cost, with a prompt's chunk the 4 head_dim operations (and one exponential)
+// per (row, position).
+//
+// Rows and items. The n G rows (new token, query head) of a sequence and cache head are cut into
+// items of at most 128 rows when there are so few, else 256: an item's rows all read the same
+// keys. A unit is a tile of 128 positions of one item. The call's units, in the order (sequence,
+// cache head, item, tile), are dealt in equal contiguous runs to one CTA per SM, so sequences
+// of any lengths balance; an item that a run's border cuts is finished by
+// attention_join_kernel from float32 partial results (at most two per CTA).
+//
+// One CTA, 10 warps:
+//  - warps 0-3 and 4-7, softmax groups 0 and 1: thread = row = TMEM lane. Group s reads its scores
+//    S_s from tensor memory, keeps m and l, writes the weights P_s (16 bits, over S_s) back, and
+//    at the end O_s to global memory. An item of 256 rows gives each group 128 rows and every
+//    tile; an item of up to 128 rows gives both groups the same rows and every other tile, and
+//    group 0 joins the two results at the end.
+//  - warp 8: deals the units, looks up pages and issues the TMA copies of K and V tiles (boxes of
+//    up to 128 slots x 64 elements, 128-byte swizzle) into a ring of stages.
+//  - warp 9, one lane: per tile S_s = Q_s K^T (both from shared memory), then O_s += P_s V (P_s
+//    from tensor memory). Q_s, written by the group, stays in shared memory for the item.
+// Tensor memory: S_0, S_1 (128 columns each, P_s over S_s), O_0, O_1 (128 columns each).
+//
+// Unseen places. Scores outside a row's range become -inf whatever they are. A weight of 0 times
+// a non-finite value would be NaN, so in a tile that some row of the item does not see in full
+// the values outside the item's range, and any with a non-finite element, are zeroed in shared
+// memory first; a row that sees a value so zeroed, or a page whose id is out of range (its TMA
+// box is filled with zeros), gives NaN.
 #pragma once
 
+#include <type_traits>
+
+#include "markov_mma.cuh"
 #include "rotary.cuh"
 
 namespace dspark {
+
+constexpr int kAtThreads = 320;
+constexpr int kAtTile = 128;        // positions per tile (and rows per softmax group)
+constexpr int kAtItemRows = 256;    // rows of an item, at most
+constexpr int kAtDescs = 4;         // items announced ahead
+constexpr int kAtBadRing = 16;      // tiles whose bad-page masks are kept
+constexpr float kAtRescale = 8.f;   // binary orders a new maximum may exceed the kept one
+
+__host__ __device__ constexpr int at_stage_bytes(int dp) { return kAtTile * dp * 2; }
+__host__ __device__ constexpr int at_stages(int dp) { return dp == 128 ? 5 : 10; }
 
 struct AttnParams {
   dspark_heads_t q, out;
@@ -12,7 +63,28 @@ struct AttnParams {
   float* lse;
   int32_t* status;
   int Hq, causal, window;
-  float scale;
+  float scale_log2;  // scale log2(e)
+  int box, box_log2; // slots per TMA box: min(page_size, 128)
+  int page_log2;
+  int part_rows;     // rows of a partial result's slot
+  float* part_o;     // [2 CTAs][part_rows][DP]
+  float2* part_ml;   // [2 CTAs][part_rows]: (c m, l)
+  struct AttnJoin* join;  // [CTAs]
+};
+
+// An item cut by a border: its first piece is in slot 2 cta + 1 of the CTA it begins in, the
+// others in slots 2 (cta + 1), 2 (cta + 2), ...; pieces == 0: nothing to join.
+struct AttnJoin {
+  int b, h, row0, rows, first, pieces;
+};
+
+// What a CTA does with one item (or its piece of it).
+struct AttnItem {
+  int b, h, row0, rows;  // the rows row0 .. row0 + rows - 1 of (sequence b, cache head h)
+  int L, n, first;       // the sequence's SeqRows
+  int t0, nt;            // tiles t0 .. t0 + nt - 1
+  int slot;              // partial result's slot; -1: the item is whole
+  int load0, tile0;      // loads and tiles that the CTA made before this item
 };
 
 // The positions [lo, hi) that new token i (of n, in a cache of L tokens) sees.
@@ -24,78 +96,858 @@ __device__ __forceinline__ void seen_range(int L, int n, int i, int causal, int 
   if (hi < lo) hi = lo;
 }
 
-// One warp per (new token, query head): 32 positions at a time, a lane scores one, the warp
-// keeps the running maximum and sum, and each lane accumulates head_dim / 32 elements.
-template <typename T>
-__global__ void __launch_bounds__(256) attention_rows_kernel(const AttnParams p) {
+// ------------------------------------------------------------------------ PTX helpers
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// 32 consecutive 32-bit columns of this warp's 32 TMEM lanes (one row per lane).
+#define DSPARK_R32(X)                                                                       \
+  X(0), X(1), X(2), X(3), X(4), X(5), X(6), X(7), X(8), X(9), X(10), X(11), X(12), X(13),   \
+      X(14), X(15), X(16), X(17), X(18), X(19), X(20), X(21), X(22), X(23), X(24), X(25),   \
+      X(26), X(27), X(28), X(29), X(30), X(31)
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+#define DSPARK_OUT(i) "=f"(v[i])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : DSPARK_R32(DSPARK_OUT)
+      : "r"(taddr)
+      : "memory");
+#undef DSPARK_OUT
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+#define DSPARK_IN(i) "r"(v[i])
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::DSPARK_R32(DSPARK_IN),
+      "r"(taddr)
+      : "memory");
+#undef DSPARK_IN
+}
+#undef DSPARK_R32
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D += A B with A (128 x 16 of 16-bit values) in tensor memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory matrix descriptor of V as the B operand of P V: element (position k, dim n) with
+// the dims contiguous (MN-major), 128-byte swizzle: atoms of 8 positions x 64 dims (1024 bytes),
+// the next 8 positions 1024 bytes on, the next 64 dims a tile's half (128 x 128 bytes) on.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
+         (static_cast<uint64_t>((kAtTile * 128) >> 4) << 16) | (64ull << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+
+// Instruction descriptor: kind::f16, A and B bf16 (bf) or f16, D float32, M = 128, N = n; B
+// K-major, or MN-major (mn).
+__host__ __device__ constexpr uint32_t at_idesc(int n, bool bf, bool mn) {
+  return (1u << 4) | (bf ? (1u << 7) | (1u << 10) : 0u) | (mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// ------------------------------------------------------------------------ units and items
+
+// Items of a (sequence, cache head) with R rows, and the tiles of an item.
+__device__ __forceinline__ int item_count(int R) {
+  return R <= kAtTile ? (R > 0) : (R + kAtItemRows - 1) / kAtItemRows;
+}
+__device__ __forceinline__ void item_tiles(const AttnParams& p, int L, int n, int G, int row0,
+                                           int rows, int& t0, int& t1) {
+  int lo, hi, lo1, hi1;
+  seen_range(L, n, row0 / G, p.causal, p.window, lo, hi1);
+  seen_range(L, n, (row0 + rows - 1) / G, p.causal, p.window, lo1, hi);
+  t0 = lo / kAtTile;
+  t1 = hi > lo ? (hi + kAtTile - 1) / kAtTile : t0;
+}
+// Units of one cache head of a sequence: its items' tiles, at least one per item.
+__device__ __forceinline__ long long head_units(const AttnParams& p, int L, int n, int G) {
+  const int R = n * G, items = item_count(R);
+  long long u = 0;
+  for (int i = 0; i < items; ++i) {
+    int t0, t1;
+    item_tiles(p, L, n, G, i * kAtItemRows, min(kAtItemRows, R - i * kAtItemRows), t0, t1);
+    u += max(1, t1 - t0);
+  }
+  return u;
+}
+
+// Loads of an item of nt tiles, in ring order: the first `look` K tiles, then V_j and K_{j+look}
+// in turn. The index of K_j and of V_j among them.
+__device__ __forceinline__ int load_of_k(int j, int look) {
+  return j < look ? j : 2 * j - look + 1;
+}
+__device__ __forceinline__ int load_of_v(int j, int look, int nt) {
+  return look + j + min(j, nt - look);
+}
+// K tiles loaded ahead of the first V: one when both groups take every tile, two when they
+// alternate.
+__device__ __forceinline__ int look_ahead(int rows, int nt) {
+  return rows > kAtTile ? 1 : min(2, nt);
+}
+
+template <int DP>
+struct AttnSmem {
+  static constexpr int kStages = at_stages(DP);
+  static constexpr int kStage = at_stage_bytes(DP);
+  static constexpr int kQ = 0;                                // [2][kStage]
+  static constexpr int kKv = 2 * kStage;                      // [kStages][kStage]
+  static constexpr int kBars = kKv + kStages * kStage;        // 64 mbarriers
+  static constexpr int kItems = kBars + 512;                  // [kAtDescs] AttnItem
+  static constexpr int kBad = kItems + kAtDescs * 48;         // [kAtBadRing][4] masks
+  static constexpr int kNf = kBad + kAtBadRing * 16;          // [3][2][4] masks
+  static constexpr int kMl = kNf + 96;                        // [128] float2
+  static constexpr int kMisc = kMl + 1024;                    // tmem base, abort, start, scan
+  static constexpr int kTotal = kMisc + 128;
+};
+static_assert(sizeof(AttnItem) == 48, "item descriptor");
+static_assert(AttnSmem<128>::kTotal <= 232448 && AttnSmem<64>::kTotal <= 232448, "shared memory");
+
+// Barriers of the CTA (indices into the 64 at kBars).
+enum AttnBar {
+  kBarFull = 0,     // [10] a stage's copy has landed (expect_tx)
+  kBarEmpty = 10,   // [10] a stage's products are done (commit)
+  kBarS = 20,       // [2] S_s is ready (commit)
+  kBarP = 22,       // [2] P_s is written (4 warps)
+  kBarO = 24,       // [2] the item's O_s is done (commit)
+  kBarQ = 26,       // [2] Q_s is written (4 warps)
+  kBarItem = 28,    // [4] an item is announced (1)
+  kBarItemFree = 32,  // [4] and read by the MMA lane and the groups' warps (1 + 8)
+  kBarFix = 36,     // [4] values zeroed: by group 0 for both groups [2], by each for itself [2]
+  kBarMl = 40,      // group 1's m and l are written (4 warps)
+  kBarJoined = 41,  // group 0 has read O_1 (4 warps)
+  kBarDrain = 42,   // the MMAs in flight at an abort
+  kBarCount = 43
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kAtThreads, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap,
+                     const __grid_constant__ AttnParams p) {
+  using Sm = AttnSmem<DP>;
+  constexpr bool kBf = sizeof(T) == 2 && !std::is_same<T, __half>::value;
+  constexpr int kStages = Sm::kStages;
+  constexpr int kHalves = DP / 64;
+  extern __shared__ __align__(1024) uint8_t at_smem[];
+  uint8_t* sm = at_smem;
+  const uint32_t sb = smem_u32(sm);
+  auto bar = [&](int i) { return sb + Sm::kBars + 8 * i; };
+  // a wait of the whole warp, with one outcome for all its lanes
+  volatile int* s_abort = reinterpret_cast<volatile int*>(sm + Sm::kMisc + 4);
+  auto wait = [&](int i, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar(i), parity & 1, s_abort)) != 0;
+  };
+  AttnItem* s_items = reinterpret_cast<AttnItem*>(sm + Sm::kItems);
+  uint32_t* s_bad = reinterpret_cast<uint32_t*>(sm + Sm::kBad);
+  uint32_t* s_nf = reinterpret_cast<uint32_t*>(sm + Sm::kNf);
+  float2* s_ml = reinterpret_cast<float2*>(sm + Sm::kMl);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + Sm::kMisc);
+  int* s_start = reinterpret_cast<int*>(sm + Sm::kMisc + 8);                 // sequence
+  long long* s_off = reinterpret_cast<long long*>(sm + Sm::kMisc + 16);      // unit within it
+  long long* s_scan = reinterpret_cast<long long*>(sm + Sm::kMisc + 24);     // [10]
+
+  const int tid = threadIdx.x, wi = tid >> 5, lane = tid & 31;
+  const dspark_kv_cache_t& c = p.cache;
+  const int Hk = c.n_heads, G = p.Hq / Hk, D = c.head_dim;
+  const int64_t cap = static_cast<int64_t>(c.max_pages) << p.page_log2;
+
+  if (tid == 0) {
+    for (int i = 0; i < kBarCount; ++i) {
+      const int count = (i >= kBarP && i < kBarO) || (i >= kBarQ && i < kBarItem) ||
+                                (i >= kBarFix && i < kBarDrain)
+                            ? 4
+                            : (i >= kBarItemFree && i < kBarFix) ? 9 : 1;
+      mbar_init(bar(i), count);
+    }
+    *s_abort = 0;
+    *s_start = -1;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+  }
+  if (wi == 9) tmem_alloc_all(s_tmem);
+  grid_dependency_wait();  // lengths, queries and the cache come from the kernels before
+  grid_dependents_launch();
+
+  // ---- this CTA's run of units: a scan of the sequences' units, a few sequences per thread
+  const int B = p.rows.B, per = (B + kAtThreads - 1) / kAtThreads;
+  const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    SeqRows s;
+    if (seq_rows(p.rows, c.kv_len, cap, b, s)) mine += Hk * head_units(p, s.L, s.n, G);
+  }
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) s_scan[wi] = upto;
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kAtThreads / 32; ++w) {
+    if (w < wi) before += s_scan[w];
+    total += s_scan[w];
+  }
+  upto += before;
+  const long long quota = (total + gridDim.x - 1) / gridDim.x;
+  const long long u0 = quota * blockIdx.x;
+  const long long u1 = min(total, u0 + quota);
+  if (u0 < u1 && u0 >= upto - mine && u0 < upto) {
+    long long off = u0 - (upto - mine);
+    for (int b = b_lo; b < b_hi; ++b) {
+      SeqRows s;
+      if (!seq_rows(p.rows, c.kv_len, cap, b, s)) continue;
+      const long long u = Hk * head_units(p, s.L, s.n, G);
+      if (off < u) {
+        *s_start = b;
+        *s_off = off;
+        break;
+      }
+      off -= u;
+    }
+  }
+  if (tid == 0) p.join[blockIdx.x].pieces = 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *s_tmem;
+
+  if (wi == 8) {
+    // ------------------------------------------------------------------ dealer and loader
+    int loads = 0, tiles = 0, items = 0;
+    bool live = true;
+    // announce an item (rows == 0: the end)
+    auto announce = [&](const AttnItem& it) {
+      const int d = items % kAtDescs;
+      if (!wait(kBarItemFree + d, (items / kAtDescs) ^ 1)) return false;
+      if (lane == 0) {
+        s_items[d] = it;
+        mbar_arrive(bar(kBarItem + d));
+      }
+      ++items;
+      return true;
+    };
+    // one stage: the K or V tile at positions 128 t .. of (b, h), the boxes that overlap [lo, hi)
+    auto load = [&](const CUtensorMap* map, const AttnItem& it, int t, int lo, int hi, int page,
+                    int idx) {
+      const int g = it.load0 + idx, st = g % kStages;
+      const int boxes = kAtTile >> p.box_log2;
+      const int x0 = t * kAtTile + (lane << p.box_log2);
+      const bool need = lane < boxes && x0 < hi && x0 + p.box > lo;
+      const uint32_t all = __ballot_sync(0xffffffffu, need);
+      if (!wait(kBarEmpty + st, (g / kStages) ^ 1)) return false;
+      if (lane == 0)
+        mbar_arrive_tx(bar(kBarFull + st),
+                       static_cast<uint32_t>(__popc(all)) * p.box * 128 * kHalves);
+      __syncwarp();
+      if (need) {
+        // a page id out of range becomes n_pages: the box is filled with zeros
+        const int pg = page >= 0 && page < c.n_pages ? page : c.n_pages;
+        const uint32_t dst = sb + Sm::kKv + st * Sm::kStage + (lane << p.box_log2) * 128;
+#pragma unroll
+        for (int hf = 0; hf < kHalves; ++hf)
+          tma_load_4d(dst + hf * (kAtTile * 128), map, 64 * hf, x0 & (c.page_size - 1), it.h, pg,
+                      bar(kBarFull + st));
+      }
+      __syncwarp();
+      loads = g + 1;
+      return true;
+    };
+    // the page id of this lane's box of tile t, or -1
+    auto page_of = [&](const AttnItem& it, int t, int lo, int hi) {
+      const int x0 = t * kAtTile + (lane << p.box_log2);
+      if (lane >= (kAtTile >> p.box_log2) || x0 >= hi || x0 + p.box <= lo) return -1;
+      return __ldg(c.page_table + it.b * c.ld_table + (x0 >> p.page_log2));
+    };
+    // the tile's mask of positions in pages out of range, for the softmax groups
+    auto note_bad = [&](int page, int t, int lo, int hi, int tile) {
+      const int x0 = t * kAtTile + (lane << p.box_log2);
+      const bool need = lane < (kAtTile >> p.box_log2) && x0 < hi && x0 + p.box > lo;
+      const uint32_t bad = __ballot_sync(0xffffffffu, need && (page < 0 || page >= c.n_pages));
+      if (lane < 4) {
+        uint32_t m = 0;
+        if (bad)
+          for (int k = 0; k < 32; ++k)
+            if ((bad >> ((32 * lane + k) >> p.box_log2)) & 1) m |= 1u << k;
+        s_bad[(tile % kAtBadRing) * 4 + lane] = m;
+      }
+      __syncwarp();
+    };
+
+    if (u0 < u1) {
+      int b = *s_start;
+      long long off = *s_off, left = u1 - u0;
+      int h = 0, i = 0;
+      bool located = false;
+      // the lanes hold the rows of 32 sequences
+      int win = -1;
+      SeqRows ws{};
+      for (; live && left > 0 && b < B; ++b) {
+        if (win < 0 || b >= win + 32) {
+          win = b;
+          ws = SeqRows{};
+          if (b + lane < B) seq_rows(p.rows, c.kv_len, cap, b + lane, ws);
+        }
+        AttnItem it;
+        it.b = b;
+        it.L = __shfl_sync(0xffffffffu, ws.L, b - win);
+        it.n = __shfl_sync(0xffffffffu, ws.n, b - win);
+        it.first = __shfl_sync(0xffffffffu, ws.first, b - win);
+        const int R = it.n * G, count = item_count(R);
+        if (count == 0) continue;
+        h = i = 0;
+        if (!located) {
+          located = true;
+          const long long hu = head_units(p, it.L, it.n, G);
+          h = static_cast<int>(off / hu);
+          off -= h * hu;
+        } else {
+          off = 0;
+        }
+        for (; live && left > 0 && h < Hk; ++h, i = 0) {
+          for (; live && left > 0 && i < count; ++i) {
+            it.h = h;
+            it.row0 = i * kAtItemRows;
+            it.rows = min(kAtItemRows, R - it.row0);
+            int t0, t1, lo, hi, x;
+            item_tiles(p, it.L, it.n, G, it.row0, it.rows, t0, t1);
+            const int u = max(1, t1 - t0);
+            if (off >= u) {  // (only while the first item is being located)
+              off -= u;
+              continue;
+            }
+            const int o = static_cast<int>(off);
+            const int take = static_cast<int>(min(static_cast<long long>(u - o), left));
+            off = 0;
+            left -= take;
+            it.t0 = t0 + o;
+            it.nt = t1 > t0 ? take : 0;
+            it.slot = o == 0 && take == u ? -1 : 2 * static_cast<int>(blockIdx.x) + (o == 0);
+            it.load0 = loads;
+            it.tile0 = tiles;
+            if (lane == 0 && o == 0 && take < u)
+              p.join[blockIdx.x] =
+                  AttnJoin{b, h, it.row0, it.rows, it.first,
+                           1 + static_cast<int>((u - take + quota - 1) / quota)};
+            live = announce(it);
+            if (!live) break;
+            if (it.nt == 0) continue;
+            seen_range(it.L, it.n, it.row0 / G, p.causal, p.window, lo, x);
+            seen_range(it.L, it.n, (it.row0 + it.rows - 1) / G, p.causal, p.window, x, hi);
+            const int look = look_ahead(it.rows, it.nt);
+            // page ids are fetched a tile before they are needed
+            int pk[3];  // ids of tiles j, j + 1, j + 2 (K runs `look` tiles ahead of V)
+            pk[0] = page_of(it, it.t0, lo, hi);
+            pk[1] = it.nt > 1 ? page_of(it, it.t0 + 1, lo, hi) : -1;
+            for (int j = 0; j < look && live; ++j) {
+              note_bad(pk[j], it.t0 + j, lo, hi, tiles + j);
+              live = load(&kmap, it, it.t0 + j, lo, hi, pk[j], j);
+            }
+            for (int j = 0; j < it.nt && live; ++j) {
+              pk[2] = j + 2 < it.nt ? page_of(it, it.t0 + j + 2, lo, hi) : -1;
+              live = load(&vmap, it, it.t0 + j, lo, hi, pk[0], load_of_v(j, look, it.nt));
+              const int jk = j + look;
+              if (live && jk < it.nt) {
+                const int page = look == 1 ? pk[1] : pk[2];
+                note_bad(page, it.t0 + jk, lo, hi, tiles + jk);
+                live = load(&kmap, it, it.t0 + jk, lo, hi, page, load_of_k(jk, look));
+              }
+              pk[0] = pk[1];
+              pk[1] = pk[2];
+            }
+            tiles += it.nt;
+          }
+        }
+      }
+    }
+    if (live) {
+      AttnItem end{};
+      announce(end);
+    }
+    if (*s_abort && lane == 0) {  // let the copies in flight land
+      for (int g = max(0, loads - kStages); g < loads; ++g)
+        drain_wait(bar(kBarFull + g % kStages), (g / kStages) & 1);
+    }
+  } else if (wi == 9) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t qk_desc = at_idesc(kAtTile, kBf, false);
+      constexpr uint32_t pv_desc = at_idesc(DP, kBf, true);
+      const int ksteps = (D + 15) / 16;
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};  // phases used of kBarQ, kBarP
+      bool live = true;
+      for (int items = 0; live; ++items) {
+        const int d = items % kAtDescs;
+        if (!mbar_wait(bar(kBarItem + d), (items / kAtDescs) & 1, s_abort)) break;
+        const int rows = s_items[d].rows, nt = s_items[d].nt, load0 = s_items[d].load0;
+        mbar_arrive(bar(kBarItemFree + d));
+        if (rows == 0) break;
+        if (nt == 0) continue;
+        const bool dual = rows > kAtTile;
+        const int look = look_ahead(rows, nt);
+        auto stage = [&](int idx) { return (load0 + idx) % kStages; };
+        auto landed = [&](int idx) {
+          return mbar_wait(bar(kBarFull + stage(idx)), ((load0 + idx) / kStages) & 1, s_abort);
+        };
+        // S_s = Q_s K_j^T
+        auto qk = [&](int s, int j) {
+          const uint32_t q0 = sb + Sm::kQ + s * Sm::kStage;
+          const uint32_t k0 = sb + Sm::kKv + stage(load_of_k(j, look)) * Sm::kStage;
+          for (int k = 0; k < ksteps; ++k) {
+            const uint32_t at = (k >> 2) * (kAtTile * 128) + 32 * (k & 3);
+            mma_f16(tbase + s * 128, sw128_desc(q0 + at), sw128_desc(k0 + at), qk_desc, k != 0);
+          }
+          mma_commit(bar(kBarS + s));
+        };
+        // O_s += P_s V_j
+        auto pv = [&](int s, int j, bool first) {
+          const uint32_t v0 =
+              sb + Sm::kKv + stage(load_of_v(j, look, nt)) * Sm::kStage;
+#pragma unroll
+          for (int k = 0; k < kAtTile / 16; ++k)
+            mma_f16_ts(tbase + 256 + s * 128, tbase + s * 128 + 8 * k,
+                       sw128_mn_desc(v0 + 2048 * k), pv_desc, !(first && k == 0));
+        };
+        auto free_stage = [&](int idx) { mma_commit(bar(kBarEmpty + stage(idx))); };
+        auto wait_q = [&](int s) {
+          if (!mbar_wait(bar(kBarQ + s), nq[s] & 1, s_abort)) return false;
+          ++nq[s];
+          return true;
+        };
+        for (int s = 0; s < 2 && live; ++s) {
+          if (!dual && s >= nt) break;
+          live = wait_q(s) && landed(load_of_k(dual ? 0 : s, look));
+          if (!live) break;
+          tc_fence_after();
+          qk(s, dual ? 0 : s);
+          if (!dual || s == 1) free_stage(load_of_k(dual ? 0 : s, look));
+        }
+        for (int j = 0; j < nt && live; ++j) {
+          live = landed(load_of_v(j, look, nt));
+          for (int s = dual ? 0 : j & 1; s < 2 && live; s += dual ? 1 : 2) {
+            live = mbar_wait(bar(kBarP + s), np[s] & 1, s_abort);
+            if (!live) break;
+            ++np[s];
+            tc_fence_after();
+            pv(s, j, dual ? j == 0 : j < 2);
+            if (!dual || s == 1) free_stage(load_of_v(j, look, nt));
+            const int jn = j + (dual ? 1 : 2);
+            if (jn < nt) {
+              live = landed(load_of_k(jn, look));
+              if (!live) break;
+              tc_fence_after();
+              qk(s, jn);
+              if (!dual || s == 1) free_stage(load_of_k(jn, look));
+            } else {
+              mma_commit(bar(kBarO + s));
+            }
+          }
+        }
+      }
+      if (*s_abort) {  // let the MMAs in flight finish
+        mma_commit(bar(kBarDrain));
+        drain_wait(bar(kBarDrain), 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax groups
+    const int s = wi >> 2, w = wi & 3, r = 32 * w + lane;  // group, TMEM quarter, lane = row
+    const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
+    const uint32_t t_s = tbase + lanes + s * 128, t_o = tbase + lanes + 256 + s * 128;
+    const float cl = p.scale_log2;
+    uint32_t n_s = 0, n_o = 0, n_pair = 0, n_fix_both = 0, n_fix_own = 0;
+    AttnItem it, next;
+    int items = 0;
+
+    // read the next announced item (rows == 0: the end); false on an abort
+    auto fetch = [&](AttnItem& to) {
+      const int d = items % kAtDescs;
+      if (!wait(kBarItem + d, items / kAtDescs)) return false;
+      to = s_items[d];
+      ++items;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarItemFree + d));
+      return true;
+    };
+    auto my_tiles = [&](const AttnItem& a) {
+      return a.rows > kAtTile ? a.nt : (a.nt - s + 1) / 2;
+    };
+    auto my_rows = [&](const AttnItem& a) {
+      return a.rows > kAtTile ? (s ? a.rows - kAtTile : kAtTile) : a.rows;
+    };
+    auto my_row0 = [&](const AttnItem& a) {
+      return a.row0 + (a.rows > kAtTile ? s * kAtTile : 0);
+    };
+    // Q_s of an item into shared memory (128-byte swizzle, K-major); elements past head_dim zero,
+    // rows past the item's left as they are (their scores are never used)
+    auto load_q = [&](const AttnItem& a) {
+      if (my_tiles(a) == 0) return;
+      constexpr int kCh = DP / 8;
+      const int rows = my_rows(a), row0 = my_row0(a);
+      uint8_t* dst = sm + Sm::kQ + s * Sm::kStage;
+      const T* q = static_cast<const T*>(p.q.p);
+#pragma unroll 4
+      for (int x = r; x < rows * kCh; x += kAtTile) {
+        const int row = x / kCh, ch = x % kCh;
+        const int token = (row0 + row) / G, g = row0 + row - token * G;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (8 * ch < D)
+          v = *reinterpret_cast<const uint4*>(q + row_offset(p.q, p.rows, a.first + token) +
+                                              (a.h * G + g) * p.q.head_stride + 8 * ch);
+        *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kAtTile * 128) + row * 128 +
+                                  (((ch & 7) ^ (row & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarQ + s));
+    };
+
+    bool live = fetch(next);
+    if (live && next.rows > 0) load_q(next);
+    while (live && next.rows > 0) {
+      it = next;
+      const bool dual = it.rows > kAtTile;
+      const int cnt = my_tiles(it), rows = my_rows(it), row0 = my_row0(it);
+      const int look = look_ahead(it.rows, it.nt);
+      const bool active = 32 * w < rows;  // some row of this warp is real
+      const bool real = r < rows;
+      const int token = (row0 + min(r, rows - 1)) / G;
+      const int g = row0 + min(r, rows - 1) - token * G;
+      int lo, hi, ilo, ihi, flo, fhi;
+      seen_range(it.L, it.n, token, p.causal, p.window, lo, hi);
+      seen_range(it.L, it.n, it.row0 / G, p.causal, p.window, ilo, fhi);
+      seen_range(it.L, it.n, (it.row0 + it.rows - 1) / G, p.causal, p.window, flo, ihi);
+      float m = -INFINITY, l = 0.f;
+      bool poison = false;
+
+      for (int k = 0; k < cnt && live; ++k) {
+        const int j = dual ? k : 2 * k + s;
+        const int x0 = (it.t0 + j) * kAtTile;
+        const bool partial = flo > x0 || fhi < x0 + kAtTile;
+        live = wait(kBarS + s, n_s);
+        if (!live) break;
+        ++n_s;
+        tc_fence_after();
+        uint32_t hit[4] = {0, 0, 0, 0};
+        {
+          const uint4 bad = *reinterpret_cast<const uint4*>(
+              s_bad + ((it.tile0 + j) % kAtBadRing) * 4);
+          hit[0] = bad.x; hit[1] = bad.y; hit[2] = bad.z; hit[3] = bad.w;
+        }
+        if (partial) {
+          // values outside the item's range, or not finite: zeroed by group 0 for both (every
+          // tile is both groups') or by the tile's own group; thread = position
+          uint32_t* nf = s_nf + ((dual ? 0 : 1 + s) * 2 + ((dual ? n_fix_both : n_fix_own) & 1)) * 4;
+          const int fix = dual ? kBarFix + (n_fix_both & 1) : kBarFix + 2 + s;
+          const uint32_t phase = dual ? n_fix_both >> 1 : n_fix_own;
+          if (!dual || s == 0) {
+            const int idx = it.load0 + load_of_v(j, look, it.nt);
+            live = wait(kBarFull + idx % kStages, idx / kStages);
+            if (!live) break;
+            uint8_t* v = sm + Sm::kKv + (idx % kStages) * Sm::kStage + r * 128;
+            const bool outside = x0 + r < ilo || x0 + r >= ihi;
+            uint32_t odd = 0;
+            if (!outside) {
+#pragma unroll
+              for (int q8 = 0; q8 < DP / 8; ++q8) {
+                const uint4 e = *reinterpret_cast<const uint4*>(
+                    v + (q8 >> 3) * (kAtTile * 128) + (((q8 & 7) ^ (r & 7)) << 4));
+                const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
+                // an element is not finite when its exponent is all ones: adding one to the
+                // exponent's last place then carries into the cleared sign bit
+                constexpr uint32_t kMag = 0x7fff7fffu, kOne = kBf ? 0x00800080u : 0x04000400u;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) odd |= ((ew[y] & kMag) + kOne) & 0x80008000u;
+              }
+            }
+            if (outside || odd) {
+#pragma unroll
+              for (int q8 = 0; q8 < DP / 8; ++q8)
+                *reinterpret_cast<uint4*>(v + (q8 >> 3) * (kAtTile * 128) +
+                                          ((q8 & 7) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+            const uint32_t word = __ballot_sync(0xffffffffu, odd != 0);
+            if (lane == 0) nf[w] = word;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(fix));
+          }
+          live = wait(fix, phase);
+          if (!live) break;
+          if (dual) ++n_fix_both; else ++n_fix_own;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) hit[y] |= nf[y];
+        }
+        if (active) {
+          float z[kAtTile];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, z + 32 * q);
+          tmem_ld_wait();
+          if (hit[0] | hit[1] | hit[2] | hit[3]) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int a = min(max(lo - x0 - 32 * y, 0), 32), e = min(max(hi - x0 - 32 * y, 0), 32);
+              const uint32_t below_e = e >= 32 ? 0xffffffffu : (1u << e) - 1;
+              const uint32_t below_a = a >= 32 ? 0xffffffffu : (1u << a) - 1;
+              if (hit[y] & below_e & ~below_a) poison = true;
+            }
+          }
+          if (partial) {
+            const int a = lo - x0, e = hi - x0;
+#pragma unroll
+            for (int q = 0; q < kAtTile; ++q)
+              if (q < a || q >= e) z[q] = -INFINITY;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int q = 0; q < kAtTile; q += 4) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], z[q + y]);
+          }
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // the kept maximum moves when the tile's exceeds it by kAtRescale binary orders
+          const bool move = real && mt > m && !((mt - m) * cl <= kAtRescale);
+          if (__any_sync(0xffffffffu, move)) {
+            const float mn = move ? mt : m;
+            const float f = move ? ex2((m - mn) * cl) : 1.f;  // m == -inf: 0
+            l *= f;
+            m = mn;
+            if (k > 0) {
+#pragma unroll
+              for (int q = 0; q < DP; q += 32) {
+                float o[32];
+                tmem_ld32(t_o + q, o);
+                tmem_ld_wait();
+                uint32_t ow[32];
+#pragma unroll
+                for (int y = 0; y < 32; ++y) ow[y] = __float_as_uint(o[y] * f);
+                tmem_st32(t_o + q, ow);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : -m * cl;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < kAtTile; q += 64) {
+            uint32_t pw[32];
+#pragma unroll
+            for (int y = 0; y < 32; ++y) {
+              const float e0 = ex2(fmaf(z[q + 2 * y], cl, base));
+              const float e1 = ex2(fmaf(z[q + 2 * y + 1], cl, base));
+              sum[y & 3] += e0 + e1;
+              pw[y] = Half16<T>::down(e0, e1);
+            }
+            tmem_st32(t_s + q / 2, pw);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarP + s));
+      }
+      if (!live) break;
+      if (poison) l = NAN;
+
+      // the item after this one: its queries, while the last products run
+      live = fetch(next);
+      if (!live) break;
+      if (next.rows > 0) load_q(next);
+
+      if (cnt > 0) {
+        live = wait(kBarO + s, n_o);
+        if (!live) break;
+        ++n_o;
+        tc_fence_after();
+      }
+      // both groups hold the same rows: group 0 takes group 1's part in
+      const bool pair = !dual && it.nt > 1;
+      float a0 = 1.f, a1 = 0.f;
+      if (pair) {
+        if (s == 1) {
+          s_ml[r] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarMl));
+        } else {
+          live = wait(kBarMl, n_pair);
+          if (!live) break;
+          tc_fence_after();
+          const float2 o = s_ml[r];
+          const float mm = fmaxf(m, o.x);
+          a0 = m == -INFINITY ? 0.f : ex2((m - mm) * cl);
+          a1 = o.x == -INFINITY ? 0.f : ex2((o.x - mm) * cl);
+          l = l * a0 + o.y * a1;
+          m = mm;
+        }
+      }
+      if (active && (dual || s == 0)) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int row = it.first + token;
+        T* out = static_cast<T*>(p.out.p) + row_offset(p.out, p.rows, row) +
+                 (it.h * G + g) * p.out.head_stride;
+        const int64_t pr = static_cast<int64_t>(it.slot) * p.part_rows + (row0 - it.row0) + r;
+#pragma unroll
+        for (int q = 0; q < DP; q += 32) {
+          float o[32];
+          if (cnt > 0) {
+            tmem_ld32(t_o + q, o);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = 0.f;
+          }
+          if (pair) {
+            float o1[32];
+            tmem_ld32(t_o + 128 + q, o1);
+            tmem_ld_wait();
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = o[y] * a0 + o1[y] * a1;
+          }
+          if (!real) {
+            // (no row of the item: the loads above still need the whole warp)
+          } else if (it.slot >= 0) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 4)
+              *reinterpret_cast<float4*>(p.part_o + pr * DP + q + y) =
+                  make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) {
+              if (q + y < D) {
+                uint4 v;
+                v.x = Half16<T>::down(o[y] * inv, o[y + 1] * inv);
+                v.y = Half16<T>::down(o[y + 2] * inv, o[y + 3] * inv);
+                v.z = Half16<T>::down(o[y + 4] * inv, o[y + 5] * inv);
+                v.w = Half16<T>::down(o[y + 6] * inv, o[y + 7] * inv);
+                *reinterpret_cast<uint4*>(out + q + y) = v;
+              }
+            }
+          }
+        }
+        if (real) {
+          if (it.slot >= 0)
+            p.part_ml[pr] = make_float2(m == -INFINITY ? m : m * cl, l);
+          else if (p.lse)
+            p.lse[static_cast<int64_t>(row) * p.Hq + it.h * G + g] =
+                l == 0.f ? -INFINITY : (m * cl + log2f(l)) * 0.69314718055994531f;
+        }
+      }
+      if (pair) {
+        tc_fence_before();
+        if (s == 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarJoined));
+        } else {
+          live = wait(kBarJoined, n_pair);
+        }
+        ++n_pair;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (wi == 9) tmem_free_all(*s_tmem);
+}
+
+// ------------------------------------------------------------------------ joining pieces
+
+// The items that a border cut, and the sequences' status. CTA (x, y): item of CTA x of the
+// attention kernel, a warp per row. With m_i (scaled to base 2), l_i and O_i of the pieces and
+// M = max m_i: out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+constexpr int kJoinWarps = 8;
+template <typename T, int DP>
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const AttnParams p) {
+  constexpr int kPer = DP / 32;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const dspark_kv_cache_t& c = p.cache;
-  const int D = c.head_dim, G = p.Hq / c.n_heads;
-  const int64_t cap = static_cast<int64_t>(c.max_pages) * c.page_size;
-  const int b = blockIdx.y;
-  SeqRows s;
-  const bool ok = seq_rows(p.rows, c.kv_len, cap, b, s);
-  if (p.status && blockIdx.x == 0 && threadIdx.x < 32) {
-    bool bad = false;
-    if (ok && s.n > 0) {
-      int lo, hi, lo1, hi1;
-      seen_range(s.L, s.n, 0, p.causal, p.window, lo, hi);
-      seen_range(s.L, s.n, s.n - 1, p.causal, p.window, lo1, hi1);
-      if (hi1 > lo)
-        for (int g = lo / c.page_size + lane; g <= (hi1 - 1) / c.page_size; g += 32) {
-          const int page = c.page_table[b * c.ld_table + g];
-          bad |= page < 0 || page >= c.n_pages;
-        }
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0) p.status[b] = !ok ? DSPARK_SEQ_BAD_PARAM : bad ? DSPARK_SEQ_BAD_PAGE : 0;
-  }
-  const int warps = gridDim.x * 8;
-  for (int w = blockIdx.x * 8 + (threadIdx.x >> 5); w < s.n * p.Hq; w += warps) {
-    const int i = w / p.Hq, h = w - i * p.Hq, row = s.first + i;
-    const T* q = static_cast<const T*>(p.q.p) + row_offset(p.q, p.rows, row) +
-                 h * p.q.head_stride;
-    const T* kb = static_cast<const T*>(c.k) + (h / G) * c.k_head_stride;
-    const T* vb = static_cast<const T*>(c.v) + (h / G) * c.v_head_stride;
-    int lo, hi;
-    seen_range(s.L, s.n, i, p.causal, p.window, lo, hi);
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int t0 = lo; t0 < hi; t0 += 32) {
-      const int t = t0 + lane;
-      float z = -INFINITY;
-      int page = 0;
+  const int G = p.Hq / c.n_heads;
+  if (p.status) {
+    const int warps = gridDim.x * gridDim.y * kJoinWarps;
+    const int64_t cap = static_cast<int64_t>(c.max_pages) << p.page_log2;
+    for (int b = (blockIdx.y * gridDim.x + blockIdx.x) * kJoinWarps + warp; b < p.rows.B;
+         b += warps) {
+      SeqRows s;
+      const bool ok = seq_rows(p.rows, c.kv_len, cap, b, s);
       bool bad = false;
-      if (t < hi) {
-        page = c.page_table[b * c.ld_table + t / c.page_size];
-        bad = page < 0 || page >= c.n_pages;
-        if (bad) page = 0;
-        const T* k = kb + page * c.k_page_stride + (t % c.page_size) * c.k_token_stride;
-        z = 0.f;
-        for (int d = 0; d < D; ++d) z += Half16<T>::up1(q[d]) * Half16<T>::up1(k[d]);
-        z *= p.scale;
-        if (bad) z = NAN;
+      if (ok && s.n > 0) {
+        int lo, hi, x;
+        seen_range(s.L, s.n, 0, p.causal, p.window, lo, x);
+        seen_range(s.L, s.n, s.n - 1, p.causal, p.window, x, hi);
+        if (hi > lo)
+          for (int g = (lo >> p.page_log2) + lane; g <= (hi - 1) >> p.page_log2; g += 32) {
+            const int page = c.page_table[b * c.ld_table + g];
+            bad |= page < 0 || page >= c.n_pages;
+          }
       }
-      const float mn = fmaxf(m, warp_max_nan(z));
-      const float mu = mn == -INFINITY ? 0.f : mn;
-      const float f = __expf(m - mu), e = __expf(z - mu);
-      l = l * f + warp_sum(e);
-      for (int d = 0; d < 4; ++d) o[d] *= f;
-      m = mn;
-      for (int j = 0; j < 32 && t0 + j < hi; ++j) {
-        const float pj = __shfl_sync(0xffffffffu, e, j);
-        const int pg = __shfl_sync(0xffffffffu, page, j);
-        const T* v = vb + pg * c.v_page_stride + ((t0 + j) % c.page_size) * c.v_token_stride;
-        for (int d = 0; d < 4; ++d)
-          if (lane + 32 * d < D) o[d] += pj * Half16<T>::up1(v[lane + 32 * d]);
-      }
+      bad = __any_sync(0xffffffffu, bad);
+      if (lane == 0) p.status[b] = !ok ? DSPARK_SEQ_BAD_PARAM : bad ? DSPARK_SEQ_BAD_PAGE : 0;
     }
-    T* out = static_cast<T*>(p.out.p) + row_offset(p.out, p.rows, row) + h * p.out.head_stride;
-    for (int d = 0; d < 4; ++d)
-      if (lane + 32 * d < D) out[lane + 32 * d] = Half16<T>::down1(l == 0.f ? 0.f : o[d] / l);
+  }
+  const AttnJoin jn = p.join[blockIdx.x];
+  if (jn.pieces == 0) return;
+  const int x = blockIdx.x;
+  for (int r = blockIdx.y * kJoinWarps + warp; r < jn.rows; r += gridDim.y * kJoinWarps) {
+    float m = -INFINITY;
+    for (int i = lane; i < jn.pieces; i += 32) {
+      const int slot = i == 0 ? 2 * x + 1 : 2 * (x + i);
+      m = fmaxf(m, p.part_ml[static_cast<int64_t>(slot) * p.part_rows + r].x);
+    }
+    m = warp_max_nan(m);
+    const float mu = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[k] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < jn.pieces; ++i) {
+      const int slot = i == 0 ? 2 * x + 1 : 2 * (x + i);
+      const int64_t pr = static_cast<int64_t>(slot) * p.part_rows + r;
+      const float2 ml = p.part_ml[pr];
+      const float a = ex2(ml.x - mu);  // -inf: 0
+      l += ml.y * a;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) o[k] += p.part_o[pr * DP + lane * kPer + k] * a;
+    }
+    const int token = (jn.row0 + r) / G, g = jn.row0 + r - token * G, row = jn.first + token;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* out = static_cast<T*>(p.out.p) + row_offset(p.out, p.rows, row) +
+             (jn.h * G + g) * p.out.head_stride;
+    if (lane * kPer < c.head_dim) {
+      if (kPer == 4)
+        *reinterpret_cast<uint2*>(out + 4 * lane) =
+            make_uint2(Half16<T>::down(o[0] * inv, o[1] * inv),
+                       Half16<T>::down(o[kPer - 2] * inv, o[kPer - 1] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(out + 2 * lane) = Half16<T>::down(o[0] * inv, o[1] * inv);
+    }
     if (p.lse && lane == 0)
-      p.lse[static_cast<int64_t>(row) * p.Hq + h] = l == 0.f ? -INFINITY : m + __logf(l);
+      p.lse[static_cast<int64_t>(row) * p.Hq + jn.h * G + g] =
+          l == 0.f ? -INFINITY : (mu + log2f(l)) * 0.69314718055994531f;
   }
 }
 

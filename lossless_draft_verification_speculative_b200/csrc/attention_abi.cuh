@@ -85,6 +85,83 @@ dspark_status_t rotary_launch(RotaryParams p, bool vec, cudaStream_t stream) {
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
+// Workspace of block_attention: the cut items, then the partial results' (m, l) and O of two
+// slots per CTA, for as many rows as an item of the call can have.
+struct AttnWs {
+  size_t join, ml, o, total;
+  int part_rows;
+};
+AttnWs attention_ws(int N, int Hq, int Hk, int D) {
+  const long long rows = static_cast<long long>(N) * (Hq / Hk);
+  AttnWs w{};
+  w.part_rows = static_cast<int>(rows < kAtItemRows ? rows : kAtItemRows);
+  const size_t slots = 2 * static_cast<size_t>(kPlanSMs) * w.part_rows;
+  w.ml = align256(sizeof(AttnJoin) * kPlanSMs);
+  w.o = w.ml + align256(slots * sizeof(float2));
+  w.total = w.o + align256(slots * (D <= 64 ? 64 : 128) * sizeof(float));
+  return w;
+}
+
+int log2_of(int pow2) {
+  int l = 0;
+  while ((1 << l) < pow2) ++l;
+  return l;
+}
+
+// The tensor map of the pages of one cache tensor: [pages][heads][slots][head_dim], boxes of
+// `box` slots x 64 elements of one head in the 128-byte swizzle; elements past head_dim, and
+// boxes of a page index past the last, are filled with zeros.
+bool page_map(CUtensorMap* map, const dspark_kv_cache_t& c, bool values, dspark_dtype_t dtype,
+              int box) {
+  const EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  const int64_t ts = values ? c.v_token_stride : c.k_token_stride;
+  const int64_t hs = values ? c.v_head_stride : c.k_head_stride;
+  const int64_t ps = values ? c.v_page_stride : c.k_page_stride;
+  const int64_t one = c.head_dim;  // any legal stride for an extent of one
+  const cuuint64_t dims[4] = {
+      static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size),
+      static_cast<cuuint64_t>(c.n_heads), static_cast<cuuint64_t>(c.n_pages)};
+  const cuuint64_t strides[3] = {2 * static_cast<cuuint64_t>(c.page_size > 1 ? ts : one),
+                                 2 * static_cast<cuuint64_t>(c.n_heads > 1 ? hs : one),
+                                 2 * static_cast<cuuint64_t>(c.n_pages > 1 ? ps : one)};
+  const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(map,
+             dtype == DSPARK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             4, values ? c.v : c.k, dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int DP>
+dspark_status_t attention_launch(AttnParams p, dspark_dtype_t dtype, const AttnWs& ws,
+                                 cudaStream_t stream) {
+  alignas(64) CUtensorMap kmap, vmap;
+  if (!page_map(&kmap, p.cache, false, dtype, p.box) ||
+      !page_map(&vmap, p.cache, true, dtype, p.box))
+    return DSPARK_ERR_UNSUPPORTED;
+  constexpr size_t smem = AttnSmem<DP>::kTotal;
+  cudaError_t e = cudaSuccess;
+  const int ctas = resident_ctas(reinterpret_cast<const void*>(&attention_kernel<T, DP>),
+                                 kAtThreads, smem, &e);
+  if (e != cudaSuccess) return DSPARK_ERR_CUDA;
+  if (ctas < 1) return DSPARK_ERR_UNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>(ctas < kPlanSMs ? ctas : kPlanSMs);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = dependent_launch(dim3(grid), kAtThreads, smem, stream, attr);
+  if (cudaLaunchKernelEx(&cfg, attention_kernel<T, DP>, kmap, vmap, p) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  // one CTA row per 8 rows of an item, at most 16 (a long item's rows take two turns)
+  const int y = (ws.part_rows + kJoinWarps - 1) / kJoinWarps;
+  cfg = dependent_launch(dim3(grid, static_cast<unsigned>(y < 1 ? 1 : y > 16 ? 16 : y)),
+                         32 * kJoinWarps, 0, stream, attr);
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP>, p) == cudaSuccess
+             ? DSPARK_OK
+             : DSPARK_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace dspark
 
@@ -175,7 +252,7 @@ size_t dspark_block_attention_workspace_bytes(int N, int n_q_heads, int n_heads,
   if (N < 0 || n_heads < 1 || n_q_heads < 1 || n_q_heads % n_heads != 0 || head_dim < 16 ||
       head_dim > 128 || head_dim % 8 != 0)
     return 0;
-  return 256;
+  return attention_ws(N, n_q_heads, n_heads, head_dim).total;
 }
 
 dspark_status_t dspark_block_attention(dspark_heads_t q, int n_q_heads, dspark_heads_t out,
@@ -197,9 +274,9 @@ dspark_status_t dspark_block_attention(dspark_heads_t q, int n_q_heads, dspark_h
   if (!heads_vec(q, rows, n_q_heads) || !heads_vec(out, rows, n_q_heads) || !cache_vec(cache) ||
       !aligned(lse, 4))
     return DSPARK_ERR_UNSUPPORTED;
-  const size_t need =
-      dspark_block_attention_workspace_bytes(rows.N, n_q_heads, cache.n_heads, D);
-  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return DSPARK_ERR_WORKSPACE;
+  const AttnWs ws = attention_ws(rows.N, n_q_heads, cache.n_heads, D);
+  if (!workspace || workspace_bytes < ws.total || !aligned(workspace, 256))
+    return DSPARK_ERR_WORKSPACE;
   AttnParams p{};
   p.q = q;
   p.out = out;
@@ -210,17 +287,22 @@ dspark_status_t dspark_block_attention(dspark_heads_t q, int n_q_heads, dspark_h
   p.Hq = n_q_heads;
   p.causal = causal != 0;
   p.window = window;
-  p.scale = scale;
+  p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  if (!std::isfinite(p.scale_log2)) return DSPARK_ERR_INVALID_ARG;
+  p.box = cache.page_size < kAtTile ? cache.page_size : kAtTile;
+  p.box_log2 = log2_of(p.box);
+  p.page_log2 = log2_of(cache.page_size);
+  char* w = static_cast<char*>(workspace);
+  p.part_rows = ws.part_rows;
+  p.join = reinterpret_cast<AttnJoin*>(w + ws.join);
+  p.part_ml = reinterpret_cast<float2*>(w + ws.ml);
+  p.part_o = reinterpret_cast<float*>(w + ws.o);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const long long warps = static_cast<long long>(rows.N) * n_q_heads;
-  const unsigned gx = static_cast<unsigned>(warps / 8 < 1 ? 1 : warps / 8 > 1024 ? 1024 : warps / 8);
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg =
-      dependent_launch(dim3(gx, static_cast<unsigned>(rows.B)), 256, 0, s, attr);
-  const cudaError_t e = dtype == DSPARK_BF16
-                            ? cudaLaunchKernelEx(&cfg, attention_rows_kernel<__nv_bfloat16>, p)
-                            : cudaLaunchKernelEx(&cfg, attention_rows_kernel<__half>, p);
-  return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  if (dtype == DSPARK_BF16)
+    return D <= 64 ? attention_launch<__nv_bfloat16, 64>(p, dtype, ws, s)
+                   : attention_launch<__nv_bfloat16, 128>(p, dtype, ws, s);
+  return D <= 64 ? attention_launch<__half, 64>(p, dtype, ws, s)
+                 : attention_launch<__half, 128>(p, dtype, ws, s);
 }
 
 }  // extern "C"
