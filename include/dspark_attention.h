@@ -58,7 +58,7 @@ typedef struct {
  * k + page * k_page_stride + slot * k_token_stride + h * k_head_stride (values likewise), so
  * [pages, slots, heads, head_dim] and [pages, heads, slots, head_dim] are both accepted.
  * kv_len[b] counts the tokens of the sequence, the new ones included: new token i sits at
- * position kv_len[b] - n + i. 0 <= kv_len[b] <= max_pages * page_size. Table entries past the
+ * position kv_len[b] - n + i. 0 <= kv_len[b] <= max_pages * page_size <= 2^30. Entries past the
  * last needed page are never read. */
 typedef struct {
   void* k;

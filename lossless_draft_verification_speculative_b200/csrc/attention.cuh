@@ -20,7 +20,7 @@
 // of any lengths balance; an item that a run's border cuts is finished by
 // attention_join_kernel from float32 partial results (at most two per CTA).
 //
-// One CTA, 10 warps:
+// One CTA, 12 warps (the last two idle):
 //  - warps 0-3 and 4-7, softmax groups 0 and 1: thread = row = TMEM lane. Group s reads its scores
 //    S_s from tensor memory, keeps m and l, writes the weights P_s (16 bits, over S_s) back, and
 //    at the end O_s to global memory. An item of 256 rows gives each group 128 rows and every
@@ -43,10 +43,14 @@
 
 #include "markov_mma.cuh"
 #include "rotary.cuh"
+#include "stream.cuh"
 
 namespace dspark {
 
-constexpr int kAtThreads = 320;
+constexpr int kAtThreads = 384;    // three warpgroups: two of softmax, one of loader and MMA issuer
+// Registers a thread: the launch gives 168; the softmax groups keep a tile's 128 scores in
+// registers and take what the third warpgroup gives up (216 + 216 + 72 = 3 x 168).
+constexpr int kAtGroupRegs = 216, kAtOtherRegs = 72;
 constexpr int kAtTile = 128;        // positions per tile (and rows per softmax group)
 constexpr int kAtItemRows = 256;    // rows of an item, at most
 constexpr int kAtDescs = 4;         // items announced ahead
@@ -63,6 +67,7 @@ struct AttnParams {
   float* lse;
   int32_t* status;
   int Hq, causal, window;
+  FastDiv by_group;  // division by the query heads of a cache head
   float scale_log2;  // scale log2(e)
   int box, box_log2; // slots per TMA box: min(page_size, 128)
   int page_log2;
@@ -134,6 +139,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
 #undef DSPARK_IN
 }
 #undef DSPARK_R32
+// mbar_wait with little code (it is inlined often, and the kernel's code should stay in the
+// instruction cache): an expired wait sets the abort flag, which the CTA counts once at its end.
+__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try(bar, parity)) return true;
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+  do {
+    if (mbar_try(bar, parity)) return true;
+  } while (!*abort && static_cast<uint32_t>(clock()) - t0 < (1u << 31));
+  *abort = 1;
+  return false;
+}
+
+// max of three; a NaN loses against a number.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -171,24 +194,37 @@ __host__ __device__ constexpr uint32_t at_idesc(int n, bool bf, bool mn) {
 __device__ __forceinline__ int item_count(int R) {
   return R <= kAtTile ? (R > 0) : (R + kAtItemRows - 1) / kAtItemRows;
 }
-__device__ __forceinline__ void item_tiles(const AttnParams& p, int L, int n, int G, int row0,
-                                           int rows, int& t0, int& t1) {
-  int lo, hi, lo1, hi1;
-  seen_range(L, n, row0 / G, p.causal, p.window, lo, hi1);
-  seen_range(L, n, (row0 + rows - 1) / G, p.causal, p.window, lo1, hi);
-  t0 = lo / kAtTile;
-  t1 = hi > lo ? (hi + kAtTile - 1) / kAtTile : t0;
+// The positions that the first and the last token of an item see: the item needs [lo, hi), and
+// every row of it sees [flo, fhi).
+struct ItemRange {
+  int lo, hi, flo, fhi;
+};
+__device__ __forceinline__ ItemRange item_range(const AttnParams& p, int L, int n, int row0,
+                                                int rows) {
+  ItemRange r;
+  seen_range(L, n, p.by_group.div(row0), p.causal, p.window, r.lo, r.fhi);
+  seen_range(L, n, p.by_group.div(row0 + rows - 1), p.causal, p.window, r.flo, r.hi);
+  return r;
+}
+__device__ __forceinline__ int first_tile(const ItemRange& r) { return r.lo / kAtTile; }
+__device__ __forceinline__ int tile_count(const ItemRange& r) {
+  return r.hi > r.lo ? (r.hi + kAtTile - 1) / kAtTile - r.lo / kAtTile : 0;
 }
 // Units of one cache head of a sequence: its items' tiles, at least one per item.
 __device__ __forceinline__ long long head_units(const AttnParams& p, int L, int n, int G) {
   const int R = n * G, items = item_count(R);
   long long u = 0;
-  for (int i = 0; i < items; ++i) {
-    int t0, t1;
-    item_tiles(p, L, n, G, i * kAtItemRows, min(kAtItemRows, R - i * kAtItemRows), t0, t1);
-    u += max(1, t1 - t0);
-  }
+#pragma unroll 1
+  for (int i = 0; i < items; ++i)
+    u += max(1, tile_count(item_range(p, L, n, i * kAtItemRows,
+                                      min(kAtItemRows, R - i * kAtItemRows))));
   return u;
+}
+// Element offset of token i of sequence b.
+__device__ __forceinline__ int64_t token_offset(const dspark_heads_t& t, const AttnParams& p,
+                                                int b, int first, int i) {
+  return p.rows.q_start ? static_cast<int64_t>(first + i) * t.token_stride
+                        : b * t.seq_stride + static_cast<int64_t>(i) * t.token_stride;
 }
 
 // Loads of an item of nt tiles, in ring order: the first `look` K tiles, then V_j and K_{j+look}
@@ -255,7 +291,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   // a wait of the whole warp, with one outcome for all its lanes
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + Sm::kMisc + 4);
   auto wait = [&](int i, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar(i), parity & 1, s_abort)) != 0;
+    return __all_sync(0xffffffffu, at_wait(bar(i), parity & 1, s_abort)) != 0;
   };
   AttnItem* s_items = reinterpret_cast<AttnItem*>(sm + Sm::kItems);
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(sm + Sm::kBad);
@@ -264,7 +300,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + Sm::kMisc);
   int* s_start = reinterpret_cast<int*>(sm + Sm::kMisc + 8);                 // sequence
   long long* s_off = reinterpret_cast<long long*>(sm + Sm::kMisc + 16);      // unit within it
-  long long* s_scan = reinterpret_cast<long long*>(sm + Sm::kMisc + 24);     // [10]
+  long long* s_scan = reinterpret_cast<long long*>(sm + Sm::kMisc + 24);     // [12]
 
   const int tid = threadIdx.x, wi = tid >> 5, lane = tid & 31;
   const dspark_kv_cache_t& c = p.cache;
@@ -335,6 +371,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   tc_fence_after();
   const uint32_t tbase = *s_tmem;
 
+  if (wi >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
   if (wi == 8) {
     // ------------------------------------------------------------------ dealer and loader
     int loads = 0, tiles = 0, items = 0;
@@ -350,51 +387,58 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       ++items;
       return true;
     };
-    // one stage: the K or V tile at positions 128 t .. of (b, h), the boxes that overlap [lo, hi)
-    auto load = [&](const CUtensorMap* map, const AttnItem& it, int t, int lo, int hi, int page,
-                    int idx) {
-      const int g = it.load0 + idx, st = g % kStages;
-      const int boxes = kAtTile >> p.box_log2;
+    // The page id of this lane's box of tile t. The lanes hold the ids of a window of 32 boxes,
+    // the one before it (V follows K by up to two tiles), and the next one, on its way.
+    int ids_before = -1, ids = -1, ids_next = -1, window = -1;
+    auto fetch_ids = [&](const AttnItem& it, int w, int hi) {
+      const int x0 = (32 * w + lane) << p.box_log2;
+      return x0 < hi ? __ldg(c.page_table + it.b * c.ld_table + (x0 >> p.page_log2)) : -1;
+    };
+    auto page_of = [&](const AttnItem& it, int t, int hi) {
+      const int box0 = t << (7 - p.box_log2), w = box0 >> 5;
+      if (window < 0 || w > window) {
+        ids_before = ids;
+        ids = window < 0 ? fetch_ids(it, w, hi) : ids_next;
+        ids_next = fetch_ids(it, w + 1, hi);
+        window = w;
+      }
+      return __shfl_sync(0xffffffffu, w == window ? ids : ids_before, (box0 + lane) & 31);
+    };
+    // one stage: the K or V tile at positions 128 t .. of (b, h), the boxes that overlap
+    // [lo, hi); with K the tile's mask of positions in pages out of range
+    auto load = [&](bool is_k, const AttnItem& it, int j, const ItemRange& rg, int idx) {
+      const int t = it.t0 + j, g = it.load0 + idx, st = g % kStages;
+      const int page = page_of(it, t, rg.hi);
       const int x0 = t * kAtTile + (lane << p.box_log2);
-      const bool need = lane < boxes && x0 < hi && x0 + p.box > lo;
+      const bool need =
+          lane < (kAtTile >> p.box_log2) && x0 < rg.hi && x0 + p.box > rg.lo;
+      const bool out = page < 0 || page >= c.n_pages;
       const uint32_t all = __ballot_sync(0xffffffffu, need);
+      const uint32_t bad = __ballot_sync(0xffffffffu, need && out);
+      if (is_k && lane < 4) {
+        uint32_t m = 0;
+        if (bad) {
+#pragma unroll 1
+          for (int k = 0; k < 32; ++k)
+            if ((bad >> ((32 * lane + k) >> p.box_log2)) & 1) m |= 1u << k;
+        }
+        s_bad[((it.tile0 + j) % kAtBadRing) * 4 + lane] = m;
+      }
       if (!wait(kBarEmpty + st, (g / kStages) ^ 1)) return false;
       if (lane == 0)
         mbar_arrive_tx(bar(kBarFull + st),
                        static_cast<uint32_t>(__popc(all)) * p.box * 128 * kHalves);
       __syncwarp();
       if (need) {
-        // a page id out of range becomes n_pages: the box is filled with zeros
-        const int pg = page >= 0 && page < c.n_pages ? page : c.n_pages;
         const uint32_t dst = sb + Sm::kKv + st * Sm::kStage + (lane << p.box_log2) * 128;
 #pragma unroll
-        for (int hf = 0; hf < kHalves; ++hf)
-          tma_load_4d(dst + hf * (kAtTile * 128), map, 64 * hf, x0 & (c.page_size - 1), it.h, pg,
-                      bar(kBarFull + st));
+        for (int hf = 0; hf < kHalves; ++hf)  // (a page index of n_pages: filled with zeros)
+          tma_load_4d(dst + hf * (kAtTile * 128), is_k ? &kmap : &vmap, 64 * hf,
+                      x0 & (c.page_size - 1), it.h, out ? c.n_pages : page, bar(kBarFull + st));
       }
       __syncwarp();
       loads = g + 1;
       return true;
-    };
-    // the page id of this lane's box of tile t, or -1
-    auto page_of = [&](const AttnItem& it, int t, int lo, int hi) {
-      const int x0 = t * kAtTile + (lane << p.box_log2);
-      if (lane >= (kAtTile >> p.box_log2) || x0 >= hi || x0 + p.box <= lo) return -1;
-      return __ldg(c.page_table + it.b * c.ld_table + (x0 >> p.page_log2));
-    };
-    // the tile's mask of positions in pages out of range, for the softmax groups
-    auto note_bad = [&](int page, int t, int lo, int hi, int tile) {
-      const int x0 = t * kAtTile + (lane << p.box_log2);
-      const bool need = lane < (kAtTile >> p.box_log2) && x0 < hi && x0 + p.box > lo;
-      const uint32_t bad = __ballot_sync(0xffffffffu, need && (page < 0 || page >= c.n_pages));
-      if (lane < 4) {
-        uint32_t m = 0;
-        if (bad)
-          for (int k = 0; k < 32; ++k)
-            if ((bad >> ((32 * lane + k) >> p.box_log2)) & 1) m |= 1u << k;
-        s_bad[(tile % kAtBadRing) * 4 + lane] = m;
-      }
-      __syncwarp();
     };
 
     if (u0 < u1) {
@@ -432,9 +476,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             it.h = h;
             it.row0 = i * kAtItemRows;
             it.rows = min(kAtItemRows, R - it.row0);
-            int t0, t1, lo, hi, x;
-            item_tiles(p, it.L, it.n, G, it.row0, it.rows, t0, t1);
-            const int u = max(1, t1 - t0);
+            const ItemRange rg = item_range(p, it.L, it.n, it.row0, it.rows);
+            const int t0 = first_tile(rg), nt = tile_count(rg), u = max(1, nt);
             if (off >= u) {  // (only while the first item is being located)
               off -= u;
               continue;
@@ -444,7 +487,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             off = 0;
             left -= take;
             it.t0 = t0 + o;
-            it.nt = t1 > t0 ? take : 0;
+            it.nt = nt > 0 ? take : 0;
             it.slot = o == 0 && take == u ? -1 : 2 * static_cast<int>(blockIdx.x) + (o == 0);
             it.load0 = loads;
             it.tile0 = tiles;
@@ -454,29 +497,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                            1 + static_cast<int>((u - take + quota - 1) / quota)};
             live = announce(it);
             if (!live) break;
-            if (it.nt == 0) continue;
-            seen_range(it.L, it.n, it.row0 / G, p.causal, p.window, lo, x);
-            seen_range(it.L, it.n, (it.row0 + it.rows - 1) / G, p.causal, p.window, x, hi);
-            const int look = look_ahead(it.rows, it.nt);
-            // page ids are fetched a tile before they are needed
-            int pk[3];  // ids of tiles j, j + 1, j + 2 (K runs `look` tiles ahead of V)
-            pk[0] = page_of(it, it.t0, lo, hi);
-            pk[1] = it.nt > 1 ? page_of(it, it.t0 + 1, lo, hi) : -1;
-            for (int j = 0; j < look && live; ++j) {
-              note_bad(pk[j], it.t0 + j, lo, hi, tiles + j);
-              live = load(&kmap, it, it.t0 + j, lo, hi, pk[j], j);
-            }
-            for (int j = 0; j < it.nt && live; ++j) {
-              pk[2] = j + 2 < it.nt ? page_of(it, it.t0 + j + 2, lo, hi) : -1;
-              live = load(&vmap, it, it.t0 + j, lo, hi, pk[0], load_of_v(j, look, it.nt));
-              const int jk = j + look;
-              if (live && jk < it.nt) {
-                const int page = look == 1 ? pk[1] : pk[2];
-                note_bad(page, it.t0 + jk, lo, hi, tiles + jk);
-                live = load(&kmap, it, it.t0 + jk, lo, hi, page, load_of_k(jk, look));
-              }
-              pk[0] = pk[1];
-              pk[1] = pk[2];
+            // in ring order (load_of_k, load_of_v)
+            const int look = look_ahead(it.rows, it.nt), more = it.nt - look;
+            window = -1;
+            for (int x = 0; x < 2 * it.nt && live; ++x) {
+              const int y = x - look;
+              const bool is_k = y < 0 || (y < 2 * more && (y & 1));
+              const int j = y < 0 ? x : y < 2 * more ? (is_k ? look : 0) + (y >> 1) : y - more;
+              live = load(is_k, it, j, rg, x);
             }
             tiles += it.nt;
           }
@@ -496,12 +524,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     if (lane == 0) {
       constexpr uint32_t qk_desc = at_idesc(kAtTile, kBf, false);
       constexpr uint32_t pv_desc = at_idesc(DP, kBf, true);
-      const int ksteps = (D + 15) / 16;
-      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};  // phases used of kBarQ, kBarP
+      uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // phases used of kBarQ, kBarP
       bool live = true;
       for (int items = 0; live; ++items) {
         const int d = items % kAtDescs;
-        if (!mbar_wait(bar(kBarItem + d), (items / kAtDescs) & 1, s_abort)) break;
+        if (!at_wait(bar(kBarItem + d), (items / kAtDescs) & 1, s_abort)) break;
         const int rows = s_items[d].rows, nt = s_items[d].nt, load0 = s_items[d].load0;
         mbar_arrive(bar(kBarItemFree + d));
         if (rows == 0) break;
@@ -510,33 +537,38 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const int look = look_ahead(rows, nt);
         auto stage = [&](int idx) { return (load0 + idx) % kStages; };
         auto landed = [&](int idx) {
-          return mbar_wait(bar(kBarFull + stage(idx)), ((load0 + idx) / kStages) & 1, s_abort);
+          return at_wait(bar(kBarFull + stage(idx)), ((load0 + idx) / kStages) & 1, s_abort);
         };
         // S_s = Q_s K_j^T
         auto qk = [&](int s, int j) {
-          const uint32_t q0 = sb + Sm::kQ + s * Sm::kStage;
-          const uint32_t k0 = sb + Sm::kKv + stage(load_of_k(j, look)) * Sm::kStage;
-          for (int k = 0; k < ksteps; ++k) {
-            const uint32_t at = (k >> 2) * (kAtTile * 128) + 32 * (k & 3);
-            mma_f16(tbase + s * 128, sw128_desc(q0 + at), sw128_desc(k0 + at), qk_desc, k != 0);
+          // (a descriptor's start address counts 16 bytes: a step of 16 dims is 2, the next 64
+          // dims a tile's half on)
+          const uint64_t q0 = sw128_desc(sb + Sm::kQ + s * Sm::kStage);
+          const uint64_t k0 =
+              sw128_desc(sb + Sm::kKv + stage(load_of_k(j, look)) * Sm::kStage);
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const int at = (k >> 2) * (kAtTile * 8) + 2 * (k & 3);
+            if (16 * k < D) mma_f16(tbase + s * 128, q0 + at, k0 + at, qk_desc, k != 0);
           }
           mma_commit(bar(kBarS + s));
         };
         // O_s += P_s V_j
         auto pv = [&](int s, int j, bool first) {
-          const uint32_t v0 =
-              sb + Sm::kKv + stage(load_of_v(j, look, nt)) * Sm::kStage;
+          const uint64_t v0 =
+              sw128_mn_desc(sb + Sm::kKv + stage(load_of_v(j, look, nt)) * Sm::kStage);
 #pragma unroll
           for (int k = 0; k < kAtTile / 16; ++k)
             mma_f16_ts(tbase + 256 + s * 128, tbase + s * 128 + 8 * k,
-                       sw128_mn_desc(v0 + 2048 * k), pv_desc, !(first && k == 0));
+                       v0 + 128 * k, pv_desc, !(first && k == 0));
         };
         auto free_stage = [&](int idx) { mma_commit(bar(kBarEmpty + stage(idx))); };
         auto wait_q = [&](int s) {
-          if (!mbar_wait(bar(kBarQ + s), nq[s] & 1, s_abort)) return false;
-          ++nq[s];
+          const uint32_t phase = s ? nq1++ : nq0++;
+          if (!at_wait(bar(kBarQ + s), phase & 1, s_abort)) return false;
           return true;
         };
+#pragma unroll 1
         for (int s = 0; s < 2 && live; ++s) {
           if (!dual && s >= nt) break;
           live = wait_q(s) && landed(load_of_k(dual ? 0 : s, look));
@@ -547,10 +579,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
         for (int j = 0; j < nt && live; ++j) {
           live = landed(load_of_v(j, look, nt));
+#pragma unroll 1
           for (int s = dual ? 0 : j & 1; s < 2 && live; s += dual ? 1 : 2) {
-            live = mbar_wait(bar(kBarP + s), np[s] & 1, s_abort);
+            const uint32_t phase = s ? np1++ : np0++;
+            live = at_wait(bar(kBarP + s), phase & 1, s_abort);
             if (!live) break;
-            ++np[s];
             tc_fence_after();
             pv(s, j, dual ? j == 0 : j < 2);
             if (!dual || s == 1) free_stage(load_of_v(j, look, nt));
@@ -572,8 +605,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         drain_wait(bar(kBarDrain), 0);
       }
     }
-  } else {
+  } else if (wi < 8) {
     // ------------------------------------------------------------------ softmax groups
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtGroupRegs));
     const int s = wi >> 2, w = wi & 3, r = 32 * w + lane;  // group, TMEM quarter, lane = row
     const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
     const uint32_t t_s = tbase + lanes + s * 128, t_o = tbase + lanes + 256 + s * 128;
@@ -609,14 +643,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const int rows = my_rows(a), row0 = my_row0(a);
       uint8_t* dst = sm + Sm::kQ + s * Sm::kStage;
       const T* q = static_cast<const T*>(p.q.p);
+      const int ch = r % kCh;
 #pragma unroll 4
-      for (int x = r; x < rows * kCh; x += kAtTile) {
-        const int row = x / kCh, ch = x % kCh;
-        const int token = (row0 + row) / G, g = row0 + row - token * G;
+      for (int row = r / kCh; row < rows; row += kAtTile / kCh) {
+        const int i = p.by_group.div(row0 + row), head = a.h * G + row0 + row - i * G;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (8 * ch < D)
-          v = *reinterpret_cast<const uint4*>(q + row_offset(p.q, p.rows, a.first + token) +
-                                              (a.h * G + g) * p.q.head_stride + 8 * ch);
+          v = *reinterpret_cast<const uint4*>(q + token_offset(p.q, p, a.b, a.first, i) +
+                                              head * p.q.head_stride + 8 * ch);
         *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kAtTile * 128) + row * 128 +
                                   (((ch & 7) ^ (row & 7)) << 4)) = v;
       }
@@ -625,28 +659,130 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       if (lane == 0) mbar_arrive(bar(kBarQ + s));
     };
 
-    bool live = fetch(next);
-    if (live && next.rows > 0) load_q(next);
-    while (live && next.rows > 0) {
+    // Per turn: the next item's queries, the results of the item before it (whose last products
+    // ran meanwhile), then the next item's tiles.
+    bool live = true, dual = false, active = false, real = false;
+    int cnt = 0, row0 = 0, token = 0, head = 0;
+    float m = -INFINITY, l = 0.f;
+    it.rows = 0;
+    while (true) {
+      live = fetch(next);
+      if (!live) break;
+      if (next.rows > 0) load_q(next);
+      if (it.rows > 0) {
+        if (cnt > 0) {
+          live = wait(kBarO + s, n_o);
+          if (!live) break;
+          ++n_o;
+          tc_fence_after();
+        }
+        // both groups hold the same rows: group 0 takes group 1's part in
+        const bool pair = !dual && it.nt > 1;
+        float a0 = 1.f, a1 = 0.f;
+        if (pair) {
+          if (s == 1) {
+            s_ml[r] = make_float2(m, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarMl));
+          } else {
+            live = wait(kBarMl, n_pair);
+            if (!live) break;
+            tc_fence_after();
+            const float2 o = s_ml[r];
+            const float mm = fmaxf(m, o.x);
+            a0 = m == -INFINITY ? 0.f : ex2((m - mm) * cl);
+            a1 = o.x == -INFINITY ? 0.f : ex2((o.x - mm) * cl);
+            l = l * a0 + o.y * a1;
+            m = mm;
+          }
+        }
+        if (active && (dual || s == 0)) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int row = it.first + token;
+          T* out = static_cast<T*>(p.out.p) + token_offset(p.out, p, it.b, it.first, token) +
+                   head * p.out.head_stride;
+          const int64_t pr = static_cast<int64_t>(it.slot) * p.part_rows + (row0 - it.row0) + r;
+          // (rolled: code that runs once an item should not push the tile's out of the
+          // instruction cache)
+#pragma unroll 1
+          for (int q = 0; q < DP; q += 32) {
+            float o[32];
+            if (cnt > 0) {
+              tmem_ld32(t_o + q, o);
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = 0.f;
+            }
+            if (pair) {
+              float o1[32];
+              tmem_ld32(t_o + 128 + q, o1);
+              tmem_ld_wait();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = o[y] * a0 + o1[y] * a1;
+            }
+            if (!real) {
+              // (no row of the item: the loads above still need the whole warp)
+            } else if (it.slot >= 0) {
+#pragma unroll
+              for (int y = 0; y < 32; y += 4)
+                *reinterpret_cast<float4*>(p.part_o + pr * DP + q + y) =
+                    make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            } else {
+#pragma unroll
+              for (int y = 0; y < 32; y += 8) {
+                if (q + y < D) {
+                  uint4 v;
+                  v.x = Half16<T>::down(o[y] * inv, o[y + 1] * inv);
+                  v.y = Half16<T>::down(o[y + 2] * inv, o[y + 3] * inv);
+                  v.z = Half16<T>::down(o[y + 4] * inv, o[y + 5] * inv);
+                  v.w = Half16<T>::down(o[y + 6] * inv, o[y + 7] * inv);
+                  *reinterpret_cast<uint4*>(out + q + y) = v;
+                }
+              }
+            }
+          }
+          if (real) {
+            if (it.slot >= 0)
+              p.part_ml[pr] = make_float2(m == -INFINITY ? m : m * cl, l);
+            else if (p.lse)
+              p.lse[static_cast<int64_t>(row) * p.Hq + head] =
+                  l == 0.f ? -INFINITY : (m * cl + log2f(l)) * 0.69314718055994531f;
+          }
+        }
+        if (pair) {
+          tc_fence_before();
+          if (s == 0) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarJoined));
+          } else {
+            live = wait(kBarJoined, n_pair);
+          }
+          ++n_pair;
+        }
+      }
+      if (next.rows == 0) break;
       it = next;
-      const bool dual = it.rows > kAtTile;
-      const int cnt = my_tiles(it), rows = my_rows(it), row0 = my_row0(it);
-      const int look = look_ahead(it.rows, it.nt);
-      const bool active = 32 * w < rows;  // some row of this warp is real
-      const bool real = r < rows;
-      const int token = (row0 + min(r, rows - 1)) / G;
-      const int g = row0 + min(r, rows - 1) - token * G;
-      int lo, hi, ilo, ihi, flo, fhi;
+      dual = it.rows > kAtTile;
+      cnt = my_tiles(it);
+      row0 = my_row0(it);
+      const int rows = my_rows(it), look = look_ahead(it.rows, it.nt);
+      active = 32 * w < rows;  // some row of this warp is real
+      real = r < rows;
+      const int mine_row = row0 + min(r, rows - 1);
+      token = p.by_group.div(mine_row);
+      head = it.h * G + mine_row - token * G;
+      int lo, hi;
       seen_range(it.L, it.n, token, p.causal, p.window, lo, hi);
-      seen_range(it.L, it.n, it.row0 / G, p.causal, p.window, ilo, fhi);
-      seen_range(it.L, it.n, (it.row0 + it.rows - 1) / G, p.causal, p.window, flo, ihi);
-      float m = -INFINITY, l = 0.f;
+      const ItemRange rg = item_range(p, it.L, it.n, it.row0, it.rows);
+      m = -INFINITY;
+      l = 0.f;
       bool poison = false;
 
       for (int k = 0; k < cnt && live; ++k) {
         const int j = dual ? k : 2 * k + s;
         const int x0 = (it.t0 + j) * kAtTile;
-        const bool partial = flo > x0 || fhi < x0 + kAtTile;
+        const bool partial = rg.flo > x0 || rg.fhi < x0 + kAtTile;
         live = wait(kBarS + s, n_s);
         if (!live) break;
         ++n_s;
@@ -668,10 +804,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             live = wait(kBarFull + idx % kStages, idx / kStages);
             if (!live) break;
             uint8_t* v = sm + Sm::kKv + (idx % kStages) * Sm::kStage + r * 128;
-            const bool outside = x0 + r < ilo || x0 + r >= ihi;
+            const bool outside = x0 + r < rg.lo || x0 + r >= rg.hi;
             uint32_t odd = 0;
             if (!outside) {
-#pragma unroll
+#pragma unroll 4
               for (int q8 = 0; q8 < DP / 8; ++q8) {
                 const uint4 e = *reinterpret_cast<const uint4*>(
                     v + (q8 >> 3) * (kAtTile * 128) + (((q8 & 7) ^ (r & 7)) << 4));
@@ -684,7 +820,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               }
             }
             if (outside || odd) {
-#pragma unroll
+#pragma unroll 4
               for (int q8 = 0; q8 < DP / 8; ++q8)
                 *reinterpret_cast<uint4*>(v + (q8 >> 3) * (kAtTile * 128) +
                                           ((q8 & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -721,13 +857,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             for (int q = 0; q < kAtTile; ++q)
               if (q < a || q >= e) z[q] = -INFINITY;
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx[4];
 #pragma unroll
-          for (int q = 0; q < kAtTile; q += 4) {
+          for (int y = 0; y < 4; ++y) mx[y] = max3(z[2 * y], z[2 * y + 1], -INFINITY);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], z[q + y]);
+          for (int q = 8; q < kAtTile; q += 8) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], z[q + 2 * y], z[q + 2 * y + 1]);
           }
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           // the kept maximum moves when the tile's exceeds it by kAtRescale binary orders
           const bool move = real && mt > m && !((mt - m) * cl <= kAtRescale);
           if (__any_sync(0xffffffffu, move)) {
@@ -736,7 +874,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             l *= f;
             m = mn;
             if (k > 0) {
-#pragma unroll
+#pragma unroll 1
               for (int q = 0; q < DP; q += 32) {
                 float o[32];
                 tmem_ld32(t_o + q, o);
@@ -749,20 +887,28 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
           }
           const float base = m == -INFINITY ? 0.f : -m * cl;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          // p = 2^(c z - c m), two at a time
+          const uint64_t c2 = pk2(cl, cl), base2 = pk2(base, base);
+          uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int q = 0; q < kAtTile; q += 64) {
             uint32_t pw[32];
 #pragma unroll
             for (int y = 0; y < 32; ++y) {
-              const float e0 = ex2(fmaf(z[q + 2 * y], cl, base));
-              const float e1 = ex2(fmaf(z[q + 2 * y + 1], cl, base));
-              sum[y & 3] += e0 + e1;
+              float e0, e1;
+              upk2(fma2(pk2(z[q + 2 * y], z[q + 2 * y + 1]), c2, base2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum[y & 3] = add2(sum[y & 3], pk2(e0, e1));
               pw[y] = Half16<T>::down(e0, e1);
             }
             tmem_st32(t_s + q / 2, pw);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          {
+            float s0, s1;
+            upk2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+            l += s0 + s1;
+          }
           tmem_st_wait();
         }
         tc_fence_before();
@@ -772,104 +918,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       if (!live) break;
       if (poison) l = NAN;
 
-      // the item after this one: its queries, while the last products run
-      live = fetch(next);
-      if (!live) break;
-      if (next.rows > 0) load_q(next);
-
-      if (cnt > 0) {
-        live = wait(kBarO + s, n_o);
-        if (!live) break;
-        ++n_o;
-        tc_fence_after();
-      }
-      // both groups hold the same rows: group 0 takes group 1's part in
-      const bool pair = !dual && it.nt > 1;
-      float a0 = 1.f, a1 = 0.f;
-      if (pair) {
-        if (s == 1) {
-          s_ml[r] = make_float2(m, l);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarMl));
-        } else {
-          live = wait(kBarMl, n_pair);
-          if (!live) break;
-          tc_fence_after();
-          const float2 o = s_ml[r];
-          const float mm = fmaxf(m, o.x);
-          a0 = m == -INFINITY ? 0.f : ex2((m - mm) * cl);
-          a1 = o.x == -INFINITY ? 0.f : ex2((o.x - mm) * cl);
-          l = l * a0 + o.y * a1;
-          m = mm;
-        }
-      }
-      if (active && (dual || s == 0)) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int row = it.first + token;
-        T* out = static_cast<T*>(p.out.p) + row_offset(p.out, p.rows, row) +
-                 (it.h * G + g) * p.out.head_stride;
-        const int64_t pr = static_cast<int64_t>(it.slot) * p.part_rows + (row0 - it.row0) + r;
-#pragma unroll
-        for (int q = 0; q < DP; q += 32) {
-          float o[32];
-          if (cnt > 0) {
-            tmem_ld32(t_o + q, o);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = 0.f;
-          }
-          if (pair) {
-            float o1[32];
-            tmem_ld32(t_o + 128 + q, o1);
-            tmem_ld_wait();
-#pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = o[y] * a0 + o1[y] * a1;
-          }
-          if (!real) {
-            // (no row of the item: the loads above still need the whole warp)
-          } else if (it.slot >= 0) {
-#pragma unroll
-            for (int y = 0; y < 32; y += 4)
-              *reinterpret_cast<float4*>(p.part_o + pr * DP + q + y) =
-                  make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
-          } else {
-#pragma unroll
-            for (int y = 0; y < 32; y += 8) {
-              if (q + y < D) {
-                uint4 v;
-                v.x = Half16<T>::down(o[y] * inv, o[y + 1] * inv);
-                v.y = Half16<T>::down(o[y + 2] * inv, o[y + 3] * inv);
-                v.z = Half16<T>::down(o[y + 4] * inv, o[y + 5] * inv);
-                v.w = Half16<T>::down(o[y + 6] * inv, o[y + 7] * inv);
-                *reinterpret_cast<uint4*>(out + q + y) = v;
-              }
-            }
-          }
-        }
-        if (real) {
-          if (it.slot >= 0)
-            p.part_ml[pr] = make_float2(m == -INFINITY ? m : m * cl, l);
-          else if (p.lse)
-            p.lse[static_cast<int64_t>(row) * p.Hq + it.h * G + g] =
-                l == 0.f ? -INFINITY : (m * cl + log2f(l)) * 0.69314718055994531f;
-        }
-      }
-      if (pair) {
-        tc_fence_before();
-        if (s == 0) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarJoined));
-        } else {
-          live = wait(kBarJoined, n_pair);
-        }
-        ++n_pair;
-      }
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *s_abort) atomicAdd(&g_pipeline_timeouts, 1ull);
   if (wi == 9) tmem_free_all(*s_tmem);
 }
 

@@ -47,7 +47,7 @@ dspark_status_t check_cache_call(const dspark_kv_cache_t& c, const dspark_rows_t
   if (c.head_dim > max_dim || Hq > 4096) return DSPARK_ERR_UNSUPPORTED;
   const long long rows = r.q_start ? r.N : static_cast<long long>(r.B) * r.N;
   if (rows * Hq > INT32_MAX || r.B > 65535 ||
-      static_cast<long long>(c.max_pages) * c.page_size > INT32_MAX - 1024)
+      static_cast<long long>(c.max_pages) * c.page_size > (1 << 30))
     return DSPARK_ERR_UNSUPPORTED;
   if (!aligned(c.k, 2) || !aligned(c.v, 2)) return DSPARK_ERR_UNSUPPORTED;
   return DSPARK_OK;
@@ -285,6 +285,7 @@ dspark_status_t dspark_block_attention(dspark_heads_t q, int n_q_heads, dspark_h
   p.lse = lse;
   p.status = status;
   p.Hq = n_q_heads;
+  p.by_group = fast_div(static_cast<uint32_t>(n_q_heads / cache.n_heads));
   p.causal = causal != 0;
   p.window = window;
   p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
