@@ -103,12 +103,47 @@ __device__ __forceinline__ void seen_range(int L, int n, int i, int causal, int 
 
 // ------------------------------------------------------------------------ PTX helpers
 
+// The loader and the MMA issuer are whole warps that follow one path, so that addresses and
+// descriptors stay in uniform registers; one elected lane issues each of these instructions.
+// (Issued from inside a one-lane branch, eight products took 75 ns each instead of 34.)
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             int z, int w, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+// D = A B (first) or D += A B, both operands in shared memory.
+__device__ __forceinline__ void at_mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same with A (128 x 16 of 16-bit values) in tensor memory.
+__device__ __forceinline__ void at_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void at_commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::
+          "r"(bar)
       : "memory");
 }
 
@@ -159,17 +194,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// D += A B with A (128 x 16 of 16-bit values) in tensor memory.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
 }
 
 // Shared-memory matrix descriptor of V as the B operand of P V: element (position k, dim n) with
@@ -302,7 +326,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   long long* s_off = reinterpret_cast<long long*>(sm + Sm::kMisc + 16);      // unit within it
   long long* s_scan = reinterpret_cast<long long*>(sm + Sm::kMisc + 24);     // [12]
 
-  const int tid = threadIdx.x, wi = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, wi = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const dspark_kv_cache_t& c = p.cache;
   const int Hk = c.n_heads, G = p.Hq / Hk, D = c.head_dim;
   const int64_t cap = static_cast<int64_t>(c.max_pages) << p.page_log2;
@@ -369,7 +393,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *s_tmem;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, *s_tmem, 0);
 
   if (wi >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
   if (wi == 8) {
@@ -429,12 +453,19 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         mbar_arrive_tx(bar(kBarFull + st),
                        static_cast<uint32_t>(__popc(all)) * p.box * 128 * kHalves);
       __syncwarp();
-      if (need) {
-        const uint32_t dst = sb + Sm::kKv + st * Sm::kStage + (lane << p.box_log2) * 128;
+      const CUtensorMap* map = is_k ? &kmap : &vmap;
+      uint32_t dst = sb + Sm::kKv + st * Sm::kStage;
+      int y = (t * kAtTile) & (c.page_size - 1);
+      if (p.box < kAtTile) y = 0;
+      const int pg = out ? c.n_pages : page;  // (a page index of n_pages: filled with zeros)
+#pragma unroll 1
+      for (int i = 0; i < (kAtTile >> p.box_log2); ++i, dst += p.box * 128) {
+        const int pi = __shfl_sync(0xffffffffu, pg, i);
+        if ((all >> i) & 1) {
 #pragma unroll
-        for (int hf = 0; hf < kHalves; ++hf)  // (a page index of n_pages: filled with zeros)
-          tma_load_4d(dst + hf * (kAtTile * 128), is_k ? &kmap : &vmap, 64 * hf,
-                      x0 & (c.page_size - 1), it.h, out ? c.n_pages : page, bar(kBarFull + st));
+          for (int hf = 0; hf < kHalves; ++hf)
+            tma_load_4d(dst + hf * (kAtTile * 128), map, 64 * hf, y, it.h, pi, bar(kBarFull + st));
+        }
       }
       __syncwarp();
       loads = g + 1;
@@ -521,23 +552,29 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
   } else if (wi == 9) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    {
       constexpr uint32_t qk_desc = at_idesc(kAtTile, kBf, false);
       constexpr uint32_t pv_desc = at_idesc(DP, kBf, true);
       uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // phases used of kBarQ, kBarP
+      int loads = 0;
       bool live = true;
       for (int items = 0; live; ++items) {
         const int d = items % kAtDescs;
-        if (!at_wait(bar(kBarItem + d), (items / kAtDescs) & 1, s_abort)) break;
-        const int rows = s_items[d].rows, nt = s_items[d].nt, load0 = s_items[d].load0;
-        mbar_arrive(bar(kBarItemFree + d));
+        if (!wait(kBarItem + d, items / kAtDescs)) break;
+        // (a shuffle from lane 0: known to be the same for all lanes)
+        const int rows = __shfl_sync(0xffffffffu, s_items[d].rows, 0);
+        const int nt = __shfl_sync(0xffffffffu, s_items[d].nt, 0);
+        const int load0 = loads;
+        loads += 2 * nt;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarItemFree + d));
         if (rows == 0) break;
         if (nt == 0) continue;
         const bool dual = rows > kAtTile;
         const int look = look_ahead(rows, nt);
         auto stage = [&](int idx) { return (load0 + idx) % kStages; };
         auto landed = [&](int idx) {
-          return at_wait(bar(kBarFull + stage(idx)), ((load0 + idx) / kStages) & 1, s_abort);
+          return wait(kBarFull + stage(idx), (load0 + idx) / kStages);
         };
         // S_s = Q_s K_j^T
         auto qk = [&](int s, int j) {
@@ -549,9 +586,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k) {
             const int at = (k >> 2) * (kAtTile * 8) + 2 * (k & 3);
-            if (16 * k < D) mma_f16(tbase + s * 128, q0 + at, k0 + at, qk_desc, k != 0);
+            if (16 * k < D) at_mma_ss(tbase + s * 128, q0 + at, k0 + at, qk_desc, k != 0);
           }
-          mma_commit(bar(kBarS + s));
+          at_commit(bar(kBarS + s));
         };
         // O_s += P_s V_j
         auto pv = [&](int s, int j, bool first) {
@@ -559,14 +596,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               sw128_mn_desc(sb + Sm::kKv + stage(load_of_v(j, look, nt)) * Sm::kStage);
 #pragma unroll
           for (int k = 0; k < kAtTile / 16; ++k)
-            mma_f16_ts(tbase + 256 + s * 128, tbase + s * 128 + 8 * k,
+            at_mma_ts(tbase + 256 + s * 128, tbase + s * 128 + 8 * k,
                        v0 + 128 * k, pv_desc, !(first && k == 0));
         };
-        auto free_stage = [&](int idx) { mma_commit(bar(kBarEmpty + stage(idx))); };
+        auto free_stage = [&](int idx) { at_commit(bar(kBarEmpty + stage(idx))); };
         auto wait_q = [&](int s) {
           const uint32_t phase = s ? nq1++ : nq0++;
-          if (!at_wait(bar(kBarQ + s), phase & 1, s_abort)) return false;
-          return true;
+          return wait(kBarQ + s, phase);
         };
 #pragma unroll 1
         for (int s = 0; s < 2 && live; ++s) {
@@ -582,7 +618,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll 1
           for (int s = dual ? 0 : j & 1; s < 2 && live; s += dual ? 1 : 2) {
             const uint32_t phase = s ? np1++ : np0++;
-            live = at_wait(bar(kBarP + s), phase & 1, s_abort);
+            live = wait(kBarP + s, phase);
             if (!live) break;
             tc_fence_after();
             pv(s, j, dual ? j == 0 : j < 2);
@@ -595,13 +631,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               qk(s, jn);
               if (!dual || s == 1) free_stage(load_of_k(jn, look));
             } else {
-              mma_commit(bar(kBarO + s));
+              at_commit(bar(kBarO + s));
             }
           }
         }
       }
       if (*s_abort) {  // let the MMAs in flight finish
-        mma_commit(bar(kBarDrain));
+        at_commit(bar(kBarDrain));
         drain_wait(bar(kBarDrain), 0);
       }
     }
