@@ -20,15 +20,17 @@
 // of any lengths balance; an item that a run's border cuts is finished by
 // attention_join_kernel from float32 partial results (at most two per CTA).
 //
-// One CTA, 12 warps (the last two idle):
+// One CTA, 12 warps:
 //  - warps 0-3 and 4-7, softmax groups 0 and 1: thread = row = TMEM lane. Group s reads its scores
 //    S_s from tensor memory, keeps m and l, writes the weights P_s (16 bits, over S_s) back, and
 //    at the end O_s to global memory. An item of 256 rows gives each group 128 rows and every
 //    tile; an item of up to 128 rows gives both groups the same rows and every other tile, and
 //    group 0 joins the two results at the end.
-//  - warp 8: deals the units, looks up pages and issues the TMA copies of K and V tiles (boxes of
-//    up to 128 slots x 64 elements, 128-byte swizzle) into a ring of stages.
-//  - warp 9, one lane: per tile S_s = Q_s K^T (both from shared memory), then O_s += P_s V (P_s
+//  - warps 8 and 10: look up pages and issue the TMA copies of the K and the V tiles (boxes of up
+//    to 128 slots x 64 elements, 128-byte swizzle) into a ring of stages; warp 8 also deals the
+//    units and announces the items.
+//  - warp 11: zeroes values that must not count (see below).
+//  - warp 9: per tile S_s = Q_s K^T (both from shared memory), then O_s += P_s V (P_s
 //    from tensor memory). Q_s, written by the group, stays in shared memory for the item.
 // Tensor memory: S_0, S_1 (128 columns each, P_s over S_s), O_0, O_1 (128 columns each).
 //
@@ -47,7 +49,7 @@
 
 namespace dspark {
 
-constexpr int kAtThreads = 384;    // three warpgroups: two of softmax, one of loader and MMA issuer
+constexpr int kAtThreads = 384;    // three warpgroups: two of softmax, one of the other roles
 // Registers a thread: the launch gives 168; the softmax groups keep a tile's 128 scores in
 // registers and take what the third warpgroup gives up (216 + 216 + 72 = 3 x 168).
 constexpr int kAtGroupRegs = 216, kAtOtherRegs = 72;
@@ -55,6 +57,7 @@ constexpr int kAtTile = 128;        // positions per tile (and rows per softmax 
 constexpr int kAtItemRows = 256;    // rows of an item, at most
 constexpr int kAtDescs = 4;         // items announced ahead
 constexpr int kAtBadRing = 16;      // tiles whose bad-page masks are kept
+constexpr int kAtFixRing = 8;       // tiles whose masks of zeroed values are kept
 constexpr float kAtRescale = 8.f;   // binary orders a new maximum may exceed the kept one
 
 __host__ __device__ constexpr int at_stage_bytes(int dp) { return kAtTile * dp * 2; }
@@ -89,7 +92,16 @@ struct AttnItem {
   int L, n, first;       // the sequence's SeqRows
   int t0, nt;            // tiles t0 .. t0 + nt - 1
   int slot;              // partial result's slot; -1: the item is whole
-  int load0, tile0;      // loads and tiles that the CTA made before this item
+  int load0;             // loads (two per tile) that the CTA made before this item
+  int lo, hi;            // positions that some row of the item sees
+  int full0, full1;      // tiles [full0, full1) are seen in full by every row
+  int fix0;              // tiles not seen in full that the CTA met before this item
+
+  __device__ __forceinline__ bool partial(int t) const { return t < full0 || t >= full1; }
+  // tiles of the piece before t that are not seen in full
+  __device__ __forceinline__ int partials_before(int t) const {
+    return t - t0 - max(0, min(t, full1) - max(t0, full0));
+  }
 };
 
 // The positions [lo, hi) that new token i (of n, in a cache of L tokens) sees.
@@ -273,30 +285,31 @@ struct AttnSmem {
   static constexpr int kKv = 2 * kStage;                      // [kStages][kStage]
   static constexpr int kBars = kKv + kStages * kStage;        // 64 mbarriers
   static constexpr int kItems = kBars + 512;                  // [kAtDescs] AttnItem
-  static constexpr int kBad = kItems + kAtDescs * 48;         // [kAtBadRing][4] masks
-  static constexpr int kNf = kBad + kAtBadRing * 16;          // [3][2][4] masks
-  static constexpr int kMl = kNf + 96;                        // [128] float2
+  static constexpr int kBad = kItems + kAtDescs * 64;         // [kAtBadRing][4] masks
+  static constexpr int kNf = kBad + kAtBadRing * 16;          // [kAtFixRing][4] masks
+  static constexpr int kMl = kNf + kAtFixRing * 16;                       // [128] float2
   static constexpr int kMisc = kMl + 1024;                    // tmem base, abort, start, scan
   static constexpr int kTotal = kMisc + 128;
 };
-static_assert(sizeof(AttnItem) == 48, "item descriptor");
+static_assert(sizeof(AttnItem) == 64, "item descriptor");
 static_assert(AttnSmem<128>::kTotal <= 232448 && AttnSmem<64>::kTotal <= 232448, "shared memory");
 
-// Barriers of the CTA (indices into the 64 at kBars).
+// Barriers of the CTA (indices into the 64 at kBars), and the arrivals each takes.
 enum AttnBar {
-  kBarFull = 0,     // [10] a stage's copy has landed (expect_tx)
-  kBarEmpty = 10,   // [10] a stage's products are done (commit)
-  kBarS = 20,       // [2] S_s is ready (commit)
-  kBarP = 22,       // [2] P_s is written (4 warps)
-  kBarO = 24,       // [2] the item's O_s is done (commit)
-  kBarQ = 26,       // [2] Q_s is written (4 warps)
-  kBarItem = 28,    // [4] an item is announced (1)
-  kBarItemFree = 32,  // [4] and read by the MMA lane and the groups' warps (1 + 8)
-  kBarFix = 36,     // [4] values zeroed: by group 0 for both groups [2], by each for itself [2]
-  kBarMl = 40,      // group 1's m and l are written (4 warps)
-  kBarJoined = 41,  // group 0 has read O_1 (4 warps)
-  kBarDrain = 42,   // the MMAs in flight at an abort
-  kBarCount = 43
+  kBarFull = 0,       // [10] a stage's copy has landed (1, expect_tx)
+  kBarEmpty = 10,     // [10] a stage's products are done (1, commit)
+  kBarS = 20,         // [2] S_s is ready (1, commit)
+  kBarO = 22,         // [2] the item's O_s is done (1, commit)
+  kBarItem = 24,      // [4] an item is announced (1)
+  kBarFix = 28,       // [8] a tile's unseen values are zeroed (1)
+  kBarToFix = 36,     // [8] the copy of such a tile is on its way (1)
+  kBarDrain = 44,     // the MMAs in flight at an abort (1, commit)
+  kBarP = 45,         // [2] P_s is written (4 warps)
+  kBarQ = 47,         // [2] Q_s is written (4 warps)
+  kBarMl = 49,        // group 1's m and l are written (4 warps)
+  kBarJoined = 50,    // group 0 has read O_1 (4 warps)
+  kBarItemFree = 51,  // [4] an item is read by the warps of all roles but the dealer (11)
+  kBarCount = 55
 };
 
 template <typename T, int DP>
@@ -332,13 +345,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const int64_t cap = static_cast<int64_t>(c.max_pages) << p.page_log2;
 
   if (tid == 0) {
-    for (int i = 0; i < kBarCount; ++i) {
-      const int count = (i >= kBarP && i < kBarO) || (i >= kBarQ && i < kBarItem) ||
-                                (i >= kBarFix && i < kBarDrain)
-                            ? 4
-                            : (i >= kBarItemFree && i < kBarFix) ? 9 : 1;
-      mbar_init(bar(i), count);
-    }
+#pragma unroll 1
+    for (int i = 0; i < kBarCount; ++i)
+      mbar_init(bar(i), i < kBarP ? 1 : i < kBarItemFree ? 4 : 11);
     *s_abort = 0;
     *s_start = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -395,91 +404,112 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   tc_fence_after();
   const uint32_t tbase = __shfl_sync(0xffffffffu, *s_tmem, 0);
 
+  // the next announced item (rows == 0: the end); false on an abort
+  int items = 0;
+  auto fetch = [&](AttnItem& to) {
+    const int d = items % kAtDescs;
+    if (!wait(kBarItem + d, items / kAtDescs)) return false;
+    to = s_items[d];
+    ++items;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarItemFree + d));
+    return true;
+  };
+
   if (wi >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
-  if (wi == 8) {
-    // ------------------------------------------------------------------ dealer and loader
-    int loads = 0, tiles = 0, items = 0;
+  if (wi == 8 || wi == 10) {
+    // ------------------------------------------------------------------ loaders
+    // Warp 8 deals the items and loads K, warp 10 loads V.
+    const bool is_k = wi == 8;
+    const CUtensorMap* map = is_k ? &kmap : &vmap;
+    const int boxes = kAtTile >> p.box_log2;
     bool live = true;
-    // announce an item (rows == 0: the end)
-    auto announce = [&](const AttnItem& it) {
-      const int d = items % kAtDescs;
-      if (!wait(kBarItemFree + d, (items / kAtDescs) ^ 1)) return false;
-      if (lane == 0) {
-        s_items[d] = it;
-        mbar_arrive(bar(kBarItem + d));
-      }
-      ++items;
-      return true;
-    };
-    // The page id of this lane's box of tile t. The lanes hold the ids of a window of 32 boxes,
-    // the one before it (V follows K by up to two tiles), and the next one, on its way.
-    int ids_before = -1, ids = -1, ids_next = -1, window = -1;
-    auto fetch_ids = [&](const AttnItem& it, int w, int hi) {
-      const int x0 = (32 * w + lane) << p.box_log2;
-      return x0 < hi ? __ldg(c.page_table + it.b * c.ld_table + (x0 >> p.page_log2)) : -1;
-    };
-    auto page_of = [&](const AttnItem& it, int t, int hi) {
-      const int box0 = t << (7 - p.box_log2), w = box0 >> 5;
-      if (window < 0 || w > window) {
-        ids_before = ids;
-        ids = window < 0 ? fetch_ids(it, w, hi) : ids_next;
-        ids_next = fetch_ids(it, w + 1, hi);
-        window = w;
-      }
-      return __shfl_sync(0xffffffffu, w == window ? ids : ids_before, (box0 + lane) & 31);
-    };
-    // one stage: the K or V tile at positions 128 t .. of (b, h), the boxes that overlap
-    // [lo, hi); with K the tile's mask of positions in pages out of range
-    auto load = [&](bool is_k, const AttnItem& it, int j, const ItemRange& rg, int idx) {
-      const int t = it.t0 + j, g = it.load0 + idx, st = g % kStages;
-      const int page = page_of(it, t, rg.hi);
-      const int x0 = t * kAtTile + (lane << p.box_log2);
-      const bool need =
-          lane < (kAtTile >> p.box_log2) && x0 < rg.hi && x0 + p.box > rg.lo;
-      const bool out = page < 0 || page >= c.n_pages;
-      const uint32_t all = __ballot_sync(0xffffffffu, need);
-      const uint32_t bad = __ballot_sync(0xffffffffu, need && out);
-      if (is_k && lane < 4) {
-        uint32_t m = 0;
-        if (bad) {
+    int last = -1;  // lane i: the last load into stage i by this warp
+    // The tiles of an item (piece). The lanes hold the page ids of a window of 32 boxes, and the
+    // next window's are on their way.
+    auto load_item = [&](const AttnItem& it) {
+      auto fetch_ids = [&](int w) {
+        const int x0 = (32 * w + lane) << p.box_log2;
+        return x0 < it.hi ? __ldg(c.page_table + it.b * c.ld_table + (x0 >> p.page_log2)) : -1;
+      };
+      const int look = look_ahead(it.rows, it.nt);
+      int window = (it.t0 << (7 - p.box_log2)) >> 5;
+      int ids = fetch_ids(window), ids_next = fetch_ids(window + 1);
 #pragma unroll 1
-          for (int k = 0; k < 32; ++k)
-            if ((bad >> ((32 * lane + k) >> p.box_log2)) & 1) m |= 1u << k;
+      for (int j = 0; j < it.nt; ++j) {
+        const int t = it.t0 + j, box0 = t << (7 - p.box_log2);
+        if ((box0 >> 5) != window) {
+          window = box0 >> 5;
+          ids = ids_next;
+          ids_next = fetch_ids(window + 1);
         }
-        s_bad[((it.tile0 + j) % kAtBadRing) * 4 + lane] = m;
-      }
-      if (!wait(kBarEmpty + st, (g / kStages) ^ 1)) return false;
-      if (lane == 0)
-        mbar_arrive_tx(bar(kBarFull + st),
-                       static_cast<uint32_t>(__popc(all)) * p.box * 128 * kHalves);
-      __syncwarp();
-      const CUtensorMap* map = is_k ? &kmap : &vmap;
-      uint32_t dst = sb + Sm::kKv + st * Sm::kStage;
-      int y = (t * kAtTile) & (c.page_size - 1);
-      if (p.box < kAtTile) y = 0;
-      const int pg = out ? c.n_pages : page;  // (a page index of n_pages: filled with zeros)
+        // the boxes that overlap [lo, hi); a page id out of range becomes n_pages, whose boxes
+        // are filled with zeros, and with K the mask of its positions is kept
+        int page = __shfl_sync(0xffffffffu, ids, (box0 + lane) & 31);
+        const int x0 = t * kAtTile + (lane << p.box_log2);
+        const bool need = lane < boxes && x0 < it.hi && x0 + p.box > it.lo;
+        const bool out = page < 0 || page >= c.n_pages;
+        const uint32_t all = __ballot_sync(0xffffffffu, need);
+        const uint32_t bad = __ballot_sync(0xffffffffu, need && out);
+        if (out) page = c.n_pages;
+        const int g = it.load0 + (is_k ? load_of_k(j, look) : load_of_v(j, look, it.nt));
+        const int st = g % kStages;
+        if (is_k && lane < 4) {
+          uint32_t m = 0;
+          if (bad) {
 #pragma unroll 1
-      for (int i = 0; i < (kAtTile >> p.box_log2); ++i, dst += p.box * 128) {
-        const int pi = __shfl_sync(0xffffffffu, pg, i);
-        if ((all >> i) & 1) {
+            for (int k = 0; k < 32; ++k)
+              if ((bad >> ((32 * lane + k) >> p.box_log2)) & 1) m |= 1u << k;
+          }
+          s_bad[((it.load0 / 2 + j) % kAtBadRing) * 4 + lane] = m;
+        }
+        if (!wait(kBarEmpty + st, (g / kStages) ^ 1)) return false;
+        if (lane == 0)
+          mbar_arrive_tx(bar(kBarFull + st),
+                         static_cast<uint32_t>(__popc(all)) * p.box * 128 * kHalves);
+        if (lane == st) last = g;
+        if (!is_k && lane == 0 && it.partial(t))
+          mbar_arrive(bar(kBarToFix + (it.fix0 + it.partials_before(t)) % kAtFixRing));
+        __syncwarp();
+        uint32_t dst = sb + Sm::kKv + st * Sm::kStage;
+        const int y = p.box < kAtTile ? 0 : (t * kAtTile) & (c.page_size - 1);
+#pragma unroll 1
+        for (int i0 = 0; i0 < boxes; i0 += 4) {
+          int pi[4];
 #pragma unroll
-          for (int hf = 0; hf < kHalves; ++hf)
-            tma_load_4d(dst + hf * (kAtTile * 128), map, 64 * hf, y, it.h, pi, bar(kBarFull + st));
+          for (int i = 0; i < 4; ++i) pi[i] = __shfl_sync(0xffffffffu, page, i0 + i);
+#pragma unroll
+          for (int i = 0; i < 4; ++i, dst += p.box * 128) {
+            if ((all >> (i0 + i)) & 1) {
+#pragma unroll
+              for (int hf = 0; hf < kHalves; ++hf)
+                tma_load_4d(dst + hf * (kAtTile * 128), map, 64 * hf, y, it.h, pi[i],
+                            bar(kBarFull + st));
+            }
+          }
         }
       }
-      __syncwarp();
-      loads = g + 1;
       return true;
     };
 
-    if (u0 < u1) {
-      int b = *s_start;
+    if (is_k) {
+      // announce an item (rows == 0: the end)
+      auto announce = [&](const AttnItem& it) {
+        const int d = items % kAtDescs;
+        if (!wait(kBarItemFree + d, (items / kAtDescs) ^ 1)) return false;
+        if (lane == 0) {
+          s_items[d] = it;
+          mbar_arrive(bar(kBarItem + d));
+        }
+        ++items;
+        return true;
+      };
+      int b = u0 < u1 ? *s_start : B, loads = 0, fixes = 0;
       long long off = *s_off, left = u1 - u0;
-      int h = 0, i = 0;
       bool located = false;
-      // the lanes hold the rows of 32 sequences
-      int win = -1;
+      int win = -1;  // the lanes hold the rows of 32 sequences
       SeqRows ws{};
+#pragma unroll 1
       for (; live && left > 0 && b < B; ++b) {
         if (win < 0 || b >= win + 32) {
           win = b;
@@ -493,62 +523,106 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         it.first = __shfl_sync(0xffffffffu, ws.first, b - win);
         const int R = it.n * G, count = item_count(R);
         if (count == 0) continue;
-        h = i = 0;
+        int h = 0;
         if (!located) {
           located = true;
           const long long hu = head_units(p, it.L, it.n, G);
           h = static_cast<int>(off / hu);
           off -= h * hu;
-        } else {
-          off = 0;
         }
-        for (; live && left > 0 && h < Hk; ++h, i = 0) {
-          for (; live && left > 0 && i < count; ++i) {
-            it.h = h;
-            it.row0 = i * kAtItemRows;
-            it.rows = min(kAtItemRows, R - it.row0);
-            const ItemRange rg = item_range(p, it.L, it.n, it.row0, it.rows);
-            const int t0 = first_tile(rg), nt = tile_count(rg), u = max(1, nt);
-            if (off >= u) {  // (only while the first item is being located)
-              off -= u;
-              continue;
-            }
-            const int o = static_cast<int>(off);
-            const int take = static_cast<int>(min(static_cast<long long>(u - o), left));
-            off = 0;
-            left -= take;
-            it.t0 = t0 + o;
-            it.nt = nt > 0 ? take : 0;
-            it.slot = o == 0 && take == u ? -1 : 2 * static_cast<int>(blockIdx.x) + (o == 0);
-            it.load0 = loads;
-            it.tile0 = tiles;
-            if (lane == 0 && o == 0 && take < u)
-              p.join[blockIdx.x] =
-                  AttnJoin{b, h, it.row0, it.rows, it.first,
-                           1 + static_cast<int>((u - take + quota - 1) / quota)};
-            live = announce(it);
-            if (!live) break;
-            // in ring order (load_of_k, load_of_v)
-            const int look = look_ahead(it.rows, it.nt), more = it.nt - look;
-            window = -1;
-            for (int x = 0; x < 2 * it.nt && live; ++x) {
-              const int y = x - look;
-              const bool is_k = y < 0 || (y < 2 * more && (y & 1));
-              const int j = y < 0 ? x : y < 2 * more ? (is_k ? look : 0) + (y >> 1) : y - more;
-              live = load(is_k, it, j, rg, x);
-            }
-            tiles += it.nt;
+#pragma unroll 1
+        for (int x = h * count; live && left > 0 && x < Hk * count; ++x) {
+          it.h = x / count;
+          it.row0 = (x - it.h * count) * kAtItemRows;
+          it.rows = min(kAtItemRows, R - it.row0);
+          const ItemRange rg = item_range(p, it.L, it.n, it.row0, it.rows);
+          const int nt = tile_count(rg), u = max(1, nt);
+          if (off >= u) {  // (only while the first item is being located)
+            off -= u;
+            continue;
           }
+          const int o = static_cast<int>(off);
+          const int take = static_cast<int>(min(static_cast<long long>(u - o), left));
+          off = 0;
+          left -= take;
+          it.t0 = first_tile(rg) + o;
+          it.nt = nt > 0 ? take : 0;
+          it.slot = o == 0 && take == u ? -1 : 2 * static_cast<int>(blockIdx.x) + (o == 0);
+          it.load0 = loads;
+          it.lo = rg.lo;
+          it.hi = rg.hi;
+          it.full0 = (rg.flo + kAtTile - 1) / kAtTile;
+          it.full1 = max(it.full0, rg.fhi / kAtTile);
+          it.fix0 = fixes;
+          loads += 2 * it.nt;
+          fixes += it.partials_before(it.t0 + it.nt);
+          if (lane == 0 && o == 0 && take < u)
+            p.join[blockIdx.x] = AttnJoin{b, it.h, it.row0, it.rows, it.first,
+                                          1 + static_cast<int>((u - take + quota - 1) / quota)};
+          live = announce(it) && load_item(it);
         }
       }
+      if (live) {
+        AttnItem end{};
+        announce(end);
+      }
+    } else {
+      AttnItem it;
+      while ((live = fetch(it)) && it.rows > 0 && (live = load_item(it))) {
+      }
     }
-    if (live) {
-      AttnItem end{};
-      announce(end);
-    }
-    if (*s_abort && lane == 0) {  // let the copies in flight land
-      for (int g = max(0, loads - kStages); g < loads; ++g)
-        drain_wait(bar(kBarFull + g % kStages), (g / kStages) & 1);
+    if (*s_abort && last >= 0)  // let the copies in flight land
+      drain_wait(bar(kBarFull + lane), (last / kStages) & 1);
+  } else if (wi == 11) {
+    // ------------------------------------------------------------------ unseen values
+    // In a tile that some row of the item does not see in full: the values outside the item's
+    // range, or with an element that is not finite, become zeros; the latter are noted.
+    AttnItem it;
+    bool live = true;
+    while (live && fetch(it) && it.rows > 0) {
+      const int look = look_ahead(it.rows, it.nt);
+      int fix = it.fix0;
+      for (int j = 0; j < it.nt && live; ++j) {
+        if (!it.partial(it.t0 + j)) continue;
+        const int g = it.load0 + load_of_v(j, look, it.nt);
+        // (first that the copy was issued: before that the stage may still hold an earlier load,
+        // whose phase a wait by parity could take for this one's)
+        live = wait(kBarToFix + fix % kAtFixRing, fix / kAtFixRing) &&
+               wait(kBarFull + g % kStages, g / kStages);
+        if (!live) break;
+#pragma unroll 1
+        for (int y = 0; y < 4; ++y) {
+          const int r = 32 * y + lane, x = (it.t0 + j) * kAtTile + r;
+          uint8_t* v = sm + Sm::kKv + (g % kStages) * Sm::kStage + r * 128;
+          const bool outside = x < it.lo || x >= it.hi;
+          uint32_t odd = 0;
+          if (!outside) {
+#pragma unroll
+            for (int q = 0; q < DP / 8; ++q) {
+              const uint4 e = *reinterpret_cast<const uint4*>(
+                  v + (q >> 3) * (kAtTile * 128) + (((q & 7) ^ (r & 7)) << 4));
+              const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
+              // an element is not finite when its exponent is all ones: adding one to the
+              // exponent's last place then carries into the cleared sign bit
+              constexpr uint32_t kMag = 0x7fff7fffu, kOne = kBf ? 0x00800080u : 0x04000400u;
+#pragma unroll
+              for (int z = 0; z < 4; ++z) odd |= ((ew[z] & kMag) + kOne) & 0x80008000u;
+            }
+          }
+          if (outside || odd) {
+#pragma unroll
+            for (int q = 0; q < DP / 8; ++q)
+              *reinterpret_cast<uint4*>(v + (q >> 3) * (kAtTile * 128) + ((q & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          const uint32_t word = __ballot_sync(0xffffffffu, odd != 0);
+          if (lane == 0) s_nf[(fix % kAtFixRing) * 4 + y] = word;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarFix + fix % kAtFixRing));
+        ++fix;
+      }
     }
   } else if (wi == 9) {
     // ------------------------------------------------------------------ MMA issuer
@@ -558,16 +632,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // phases used of kBarQ, kBarP
       int loads = 0;
       bool live = true;
-      for (int items = 0; live; ++items) {
-        const int d = items % kAtDescs;
-        if (!wait(kBarItem + d, items / kAtDescs)) break;
+      AttnItem it;
+      while (live && fetch(it)) {
         // (a shuffle from lane 0: known to be the same for all lanes)
-        const int rows = __shfl_sync(0xffffffffu, s_items[d].rows, 0);
-        const int nt = __shfl_sync(0xffffffffu, s_items[d].nt, 0);
+        const int rows = __shfl_sync(0xffffffffu, it.rows, 0);
+        const int nt = __shfl_sync(0xffffffffu, it.nt, 0);
         const int load0 = loads;
         loads += 2 * nt;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarItemFree + d));
         if (rows == 0) break;
         if (nt == 0) continue;
         const bool dual = rows > kAtTile;
@@ -615,6 +686,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
         for (int j = 0; j < nt && live; ++j) {
           live = landed(load_of_v(j, look, nt));
+          if (live && it.partial(it.t0 + j)) {
+            const int fix = it.fix0 + it.partials_before(it.t0 + j);
+            live = wait(kBarFix + fix % kAtFixRing, fix / kAtFixRing);
+          }
 #pragma unroll 1
           for (int s = dual ? 0 : j & 1; s < 2 && live; s += dual ? 1 : 2) {
             const uint32_t phase = s ? np1++ : np0++;
@@ -648,20 +723,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
     const uint32_t t_s = tbase + lanes + s * 128, t_o = tbase + lanes + 256 + s * 128;
     const float cl = p.scale_log2;
-    uint32_t n_s = 0, n_o = 0, n_pair = 0, n_fix_both = 0, n_fix_own = 0;
+    uint32_t n_s = 0, n_o = 0, n_pair = 0;
     AttnItem it, next;
-    int items = 0;
 
-    // read the next announced item (rows == 0: the end); false on an abort
-    auto fetch = [&](AttnItem& to) {
-      const int d = items % kAtDescs;
-      if (!wait(kBarItem + d, items / kAtDescs)) return false;
-      to = s_items[d];
-      ++items;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarItemFree + d));
-      return true;
-    };
     auto my_tiles = [&](const AttnItem& a) {
       return a.rows > kAtTile ? a.nt : (a.nt - s + 1) / 2;
     };
@@ -802,7 +866,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       dual = it.rows > kAtTile;
       cnt = my_tiles(it);
       row0 = my_row0(it);
-      const int rows = my_rows(it), look = look_ahead(it.rows, it.nt);
+      const int rows = my_rows(it);
       active = 32 * w < rows;  // some row of this warp is real
       real = r < rows;
       const int mine_row = row0 + min(r, rows - 1);
@@ -810,7 +874,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       head = it.h * G + mine_row - token * G;
       int lo, hi;
       seen_range(it.L, it.n, token, p.causal, p.window, lo, hi);
-      const ItemRange rg = item_range(p, it.L, it.n, it.row0, it.rows);
       m = -INFINITY;
       l = 0.f;
       bool poison = false;
@@ -818,75 +881,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       for (int k = 0; k < cnt && live; ++k) {
         const int j = dual ? k : 2 * k + s;
         const int x0 = (it.t0 + j) * kAtTile;
-        const bool partial = rg.flo > x0 || rg.fhi < x0 + kAtTile;
+        const bool partial = it.partial(it.t0 + j);
         live = wait(kBarS + s, n_s);
         if (!live) break;
         ++n_s;
         tc_fence_after();
-        uint32_t hit[4] = {0, 0, 0, 0};
-        {
-          const uint4 bad = *reinterpret_cast<const uint4*>(
-              s_bad + ((it.tile0 + j) % kAtBadRing) * 4);
-          hit[0] = bad.x; hit[1] = bad.y; hit[2] = bad.z; hit[3] = bad.w;
-        }
-        if (partial) {
-          // values outside the item's range, or not finite: zeroed by group 0 for both (every
-          // tile is both groups') or by the tile's own group; thread = position
-          uint32_t* nf = s_nf + ((dual ? 0 : 1 + s) * 2 + ((dual ? n_fix_both : n_fix_own) & 1)) * 4;
-          const int fix = dual ? kBarFix + (n_fix_both & 1) : kBarFix + 2 + s;
-          const uint32_t phase = dual ? n_fix_both >> 1 : n_fix_own;
-          if (!dual || s == 0) {
-            const int idx = it.load0 + load_of_v(j, look, it.nt);
-            live = wait(kBarFull + idx % kStages, idx / kStages);
-            if (!live) break;
-            uint8_t* v = sm + Sm::kKv + (idx % kStages) * Sm::kStage + r * 128;
-            const bool outside = x0 + r < rg.lo || x0 + r >= rg.hi;
-            uint32_t odd = 0;
-            if (!outside) {
-#pragma unroll 4
-              for (int q8 = 0; q8 < DP / 8; ++q8) {
-                const uint4 e = *reinterpret_cast<const uint4*>(
-                    v + (q8 >> 3) * (kAtTile * 128) + (((q8 & 7) ^ (r & 7)) << 4));
-                const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
-                // an element is not finite when its exponent is all ones: adding one to the
-                // exponent's last place then carries into the cleared sign bit
-                constexpr uint32_t kMag = 0x7fff7fffu, kOne = kBf ? 0x00800080u : 0x04000400u;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) odd |= ((ew[y] & kMag) + kOne) & 0x80008000u;
-              }
-            }
-            if (outside || odd) {
-#pragma unroll 4
-              for (int q8 = 0; q8 < DP / 8; ++q8)
-                *reinterpret_cast<uint4*>(v + (q8 >> 3) * (kAtTile * 128) +
-                                          ((q8 & 7) << 4)) = make_uint4(0, 0, 0, 0);
-            }
-            const uint32_t word = __ballot_sync(0xffffffffu, odd != 0);
-            if (lane == 0) nf[w] = word;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(fix));
-          }
-          live = wait(fix, phase);
-          if (!live) break;
-          if (dual) ++n_fix_both; else ++n_fix_own;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) hit[y] |= nf[y];
-        }
         if (active) {
           float z[kAtTile];
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, z + 32 * q);
           tmem_ld_wait();
-          if (hit[0] | hit[1] | hit[2] | hit[3]) {
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int a = min(max(lo - x0 - 32 * y, 0), 32), e = min(max(hi - x0 - 32 * y, 0), 32);
-              const uint32_t below_e = e >= 32 ? 0xffffffffu : (1u << e) - 1;
-              const uint32_t below_a = a >= 32 ? 0xffffffffu : (1u << a) - 1;
-              if (hit[y] & below_e & ~below_a) poison = true;
-            }
-          }
           if (partial) {
             const int a = lo - x0, e = hi - x0;
 #pragma unroll
@@ -950,6 +954,26 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarP + s));
+        // positions in a page out of range, or whose value was not finite and is now zero
+        uint4 hit = *reinterpret_cast<const uint4*>(
+            s_bad + ((it.load0 / 2 + j) % kAtBadRing) * 4);
+        if (partial) {
+          const int fix = it.fix0 + it.partials_before(it.t0 + j);
+          live = wait(kBarFix + fix % kAtFixRing, fix / kAtFixRing);
+          if (!live) break;
+          const uint4 nf = *reinterpret_cast<const uint4*>(s_nf + (fix % kAtFixRing) * 4);
+          hit.x |= nf.x;
+          hit.y |= nf.y;
+          hit.z |= nf.z;
+          hit.w |= nf.w;
+        }
+        if (hit.x | hit.y | hit.z | hit.w) {
+#pragma unroll 1
+          for (int q = max(lo - x0, 0); q < min(hi - x0, kAtTile); ++q) {
+            const uint32_t word = q < 64 ? (q < 32 ? hit.x : hit.y) : (q < 96 ? hit.z : hit.w);
+            if ((word >> (q & 31)) & 1) poison = true;
+          }
+        }
       }
       if (!live) break;
       if (poison) l = NAN;
