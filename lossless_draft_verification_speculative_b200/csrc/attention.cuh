@@ -25,7 +25,7 @@
 //    S_s from tensor memory, keeps m and l, writes the weights P_s (16 bits, over S_s) back, and
 //    at the end O_s to global memory. An item of 256 rows gives each group 128 rows and every
 //    tile; an item of up to 128 rows gives both groups the same rows and every other tile, and
-//    group 0 joins the two results at the end.
+//    the group of the first tile (they take turns at that) joins the two results at the end.
 //  - warps 8 and 10: look up pages and issue the TMA copies of the K and the V tiles (boxes of up
 //    to 128 slots x 64 elements, 128-byte swizzle) into a ring of stages; warp 8 also deals the
 //    units and announces the items.
@@ -306,8 +306,8 @@ enum AttnBar {
   kBarDrain = 44,     // the MMAs in flight at an abort (1, commit)
   kBarP = 45,         // [2] P_s is written (4 warps)
   kBarQ = 47,         // [2] Q_s is written (4 warps)
-  kBarMl = 49,        // group 1's m and l are written (4 warps)
-  kBarJoined = 50,    // group 0 has read O_1 (4 warps)
+  kBarMl = 49,        // the other group's m and l are written (4 warps)
+  kBarJoined = 50,    // and its O is read (4 warps)
   kBarItemFree = 51,  // [4] an item is read by the warps of all roles but the dealer (11)
   kBarCount = 55
 };
@@ -425,23 +425,25 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int boxes = kAtTile >> p.box_log2;
     bool live = true;
     int last = -1;  // lane i: the last load into stage i by this warp
-    // The tiles of an item (piece). The lanes hold the page ids of a window of 32 boxes, and the
-    // next window's are on their way.
-    auto load_item = [&](const AttnItem& it) {
-      auto fetch_ids = [&](int w) {
-        const int x0 = (32 * w + lane) << p.box_log2;
-        return x0 < it.hi ? __ldg(c.page_table + it.b * c.ld_table + (x0 >> p.page_log2)) : -1;
-      };
+    // The lanes hold the page ids of a window of 32 boxes; the next window's, and those of the
+    // next item's first window, are on their way.
+    auto fetch_ids = [&](const AttnItem& it, int w) {
+      const int x0 = (32 * w + lane) << p.box_log2;
+      return x0 < it.hi ? __ldg(c.page_table + it.b * c.ld_table + (x0 >> p.page_log2)) : -1;
+    };
+    auto first_window = [&](const AttnItem& it) { return (it.t0 << (7 - p.box_log2)) >> 5; };
+    // the tiles of an item (piece)
+    auto load_item = [&](const AttnItem& it, int ids) {
       const int look = look_ahead(it.rows, it.nt);
-      int window = (it.t0 << (7 - p.box_log2)) >> 5;
-      int ids = fetch_ids(window), ids_next = fetch_ids(window + 1);
+      int window = first_window(it);
+      int ids_next = fetch_ids(it, window + 1);
 #pragma unroll 1
       for (int j = 0; j < it.nt; ++j) {
         const int t = it.t0 + j, box0 = t << (7 - p.box_log2);
         if ((box0 >> 5) != window) {
           window = box0 >> 5;
           ids = ids_next;
-          ids_next = fetch_ids(window + 1);
+          ids_next = fetch_ids(it, window + 1);
         }
         // the boxes that overlap [lo, hi); a page id out of range becomes n_pages, whose boxes
         // are filled with zeros, and with K the mask of its positions is kept
@@ -509,6 +511,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       bool located = false;
       int win = -1;  // the lanes hold the rows of 32 sequences
       SeqRows ws{};
+      AttnItem now;  // the item to load: the one before the last announced
+      now.rows = 0;
+      int ids_now = -1;
 #pragma unroll 1
       for (; live && left > 0 && b < B; ++b) {
         if (win < 0 || b >= win + 32) {
@@ -559,16 +564,28 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           if (lane == 0 && o == 0 && take < u)
             p.join[blockIdx.x] = AttnJoin{b, it.h, it.row0, it.rows, it.first,
                                           1 + static_cast<int>((u - take + quota - 1) / quota)};
-          live = announce(it) && load_item(it);
+          live = announce(it);
+          const int ids = fetch_ids(it, first_window(it));
+          if (live && now.rows > 0) live = load_item(now, ids_now);
+          now = it;
+          ids_now = ids;
         }
       }
       if (live) {
         AttnItem end{};
-        announce(end);
+        live = announce(end);
       }
+      if (live && now.rows > 0) load_item(now, ids_now);
     } else {
-      AttnItem it;
-      while ((live = fetch(it)) && it.rows > 0 && (live = load_item(it))) {
+      AttnItem now, it;
+      now.rows = 0;
+      int ids_now = -1;
+      while (live && fetch(it)) {
+        const int ids = it.rows > 0 ? fetch_ids(it, first_window(it)) : -1;
+        if (now.rows > 0) live = load_item(now, ids_now);
+        if (it.rows == 0) break;
+        now = it;
+        ids_now = ids;
       }
     }
     if (*s_abort && last >= 0)  // let the copies in flight land
@@ -642,6 +659,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (rows == 0) break;
         if (nt == 0) continue;
         const bool dual = rows > kAtTile;
+        const int flip = (items - 1) & 1;  // the group that takes tile 0 (see the groups)
         const int look = look_ahead(rows, nt);
         auto stage = [&](int idx) { return (load0 + idx) % kStages; };
         auto landed = [&](int idx) {
@@ -676,13 +694,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           return wait(kBarQ + s, phase);
         };
 #pragma unroll 1
-        for (int s = 0; s < 2 && live; ++s) {
-          if (!dual && s >= nt) break;
-          live = wait_q(s) && landed(load_of_k(dual ? 0 : s, look));
+        for (int x = 0; x < (dual ? 2 : min(2, nt)) && live; ++x) {
+          const int s = dual ? x : x ^ flip, j = dual ? 0 : x;
+          live = wait_q(s) && landed(load_of_k(j, look));
           if (!live) break;
           tc_fence_after();
-          qk(s, dual ? 0 : s);
-          if (!dual || s == 1) free_stage(load_of_k(dual ? 0 : s, look));
+          qk(s, j);
+          if (!dual || x == 1) free_stage(load_of_k(j, look));
         }
         for (int j = 0; j < nt && live; ++j) {
           live = landed(load_of_v(j, look, nt));
@@ -691,20 +709,21 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             live = wait(kBarFix + fix % kAtFixRing, fix / kAtFixRing);
           }
 #pragma unroll 1
-          for (int s = dual ? 0 : j & 1; s < 2 && live; s += dual ? 1 : 2) {
+          for (int x = dual ? 0 : 1; x < 2 && live; ++x) {
+            const int s = dual ? x : (j & 1) ^ flip;
             const uint32_t phase = s ? np1++ : np0++;
             live = wait(kBarP + s, phase);
             if (!live) break;
             tc_fence_after();
             pv(s, j, dual ? j == 0 : j < 2);
-            if (!dual || s == 1) free_stage(load_of_v(j, look, nt));
+            if (x == 1) free_stage(load_of_v(j, look, nt));
             const int jn = j + (dual ? 1 : 2);
             if (jn < nt) {
               live = landed(load_of_k(jn, look));
               if (!live) break;
               tc_fence_after();
               qk(s, jn);
-              if (!dual || s == 1) free_stage(load_of_k(jn, look));
+              if (x == 1) free_stage(load_of_k(jn, look));
             } else {
               at_commit(bar(kBarO + s));
             }
@@ -722,12 +741,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int s = wi >> 2, w = wi & 3, r = 32 * w + lane;  // group, TMEM quarter, lane = row
     const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
     const uint32_t t_s = tbase + lanes + s * 128, t_o = tbase + lanes + 256 + s * 128;
+    const uint32_t t_other = tbase + lanes + 256 + (s ^ 1) * 128;
     const float cl = p.scale_log2;
     uint32_t n_s = 0, n_o = 0, n_pair = 0;
+    bool owed = false;        // the other group may still be reading this group's O
+    uint32_t owed_phase = 0;
     AttnItem it, next;
+    int rel = 0, rel_next = 0;  // items of up to 128 rows: this group takes tiles rel, rel + 2, ..
 
-    auto my_tiles = [&](const AttnItem& a) {
-      return a.rows > kAtTile ? a.nt : (a.nt - s + 1) / 2;
+    auto my_tiles = [&](const AttnItem& a, int first) {
+      return a.rows > kAtTile ? a.nt : (a.nt - first + 1) / 2;
     };
     auto my_rows = [&](const AttnItem& a) {
       return a.rows > kAtTile ? (s ? a.rows - kAtTile : kAtTile) : a.rows;
@@ -738,7 +761,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     // Q_s of an item into shared memory (128-byte swizzle, K-major); elements past head_dim zero,
     // rows past the item's left as they are (their scores are never used)
     auto load_q = [&](const AttnItem& a) {
-      if (my_tiles(a) == 0) return;
+      if (my_tiles(a, rel_next) == 0) return;
       constexpr int kCh = DP / 8;
       const int rows = my_rows(a), row0 = my_row0(a);
       uint8_t* dst = sm + Sm::kQ + s * Sm::kStage;
@@ -768,6 +791,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     while (true) {
       live = fetch(next);
       if (!live) break;
+      rel_next = s ^ ((items - 1) & 1);  // short items alternate between the groups
       if (next.rows > 0) load_q(next);
       if (it.rows > 0) {
         if (cnt > 0) {
@@ -776,11 +800,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           ++n_o;
           tc_fence_after();
         }
-        // both groups hold the same rows: group 0 takes group 1's part in
+        // both groups hold the same rows: the one of tile 0 takes the other's part in
         const bool pair = !dual && it.nt > 1;
         float a0 = 1.f, a1 = 0.f;
         if (pair) {
-          if (s == 1) {
+          if (rel == 1) {
             s_ml[r] = make_float2(m, l);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarMl));
@@ -796,7 +820,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             m = mm;
           }
         }
-        if (active && (dual || s == 0)) {
+        if (active && (dual || rel == 0)) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const int row = it.first + token;
           T* out = static_cast<T*>(p.out.p) + token_offset(p.out, p, it.b, it.first, token) +
@@ -816,7 +840,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
             if (pair) {
               float o1[32];
-              tmem_ld32(t_o + 128 + q, o1);
+              tmem_ld32(t_other + q, o1);
               tmem_ld_wait();
 #pragma unroll
               for (int y = 0; y < 32; ++y) o[y] = o[y] * a0 + o1[y] * a1;
@@ -851,20 +875,22 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
         }
         if (pair) {
-          tc_fence_before();
-          if (s == 0) {
+          if (rel == 0) {
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarJoined));
           } else {
-            live = wait(kBarJoined, n_pair);
+            owed = true;
+            owed_phase = n_pair;
           }
           ++n_pair;
         }
       }
       if (next.rows == 0) break;
       it = next;
+      rel = rel_next;
       dual = it.rows > kAtTile;
-      cnt = my_tiles(it);
+      cnt = my_tiles(it, rel);
       row0 = my_row0(it);
       const int rows = my_rows(it);
       active = 32 * w < rows;  // some row of this warp is real
@@ -879,7 +905,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       bool poison = false;
 
       for (int k = 0; k < cnt && live; ++k) {
-        const int j = dual ? k : 2 * k + s;
+        const int j = dual ? k : 2 * k + rel;
         const int x0 = (it.t0 + j) * kAtTile;
         const bool partial = it.partial(it.t0 + j);
         live = wait(kBarS + s, n_s);
@@ -950,6 +976,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             l += s0 + s1;
           }
           tmem_st_wait();
+        }
+        if (owed) {  // before this group's O may be written again
+          live = wait(kBarJoined, owed_phase);
+          if (!live) break;
+          owed = false;
         }
         tc_fence_before();
         __syncwarp();
