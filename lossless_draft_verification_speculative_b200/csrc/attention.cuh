@@ -494,99 +494,99 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       return true;
     };
 
-    if (is_k) {
-      // announce an item (rows == 0: the end)
-      auto announce = [&](const AttnItem& it) {
-        const int d = items % kAtDescs;
-        if (!wait(kBarItemFree + d, (items / kAtDescs) ^ 1)) return false;
-        if (lane == 0) {
-          s_items[d] = it;
-          mbar_arrive(bar(kBarItem + d));
-        }
-        ++items;
-        return true;
-      };
-      int b = u0 < u1 ? *s_start : B, loads = 0, fixes = 0;
-      long long off = *s_off, left = u1 - u0;
-      bool located = false;
-      int win = -1;  // the lanes hold the rows of 32 sequences
-      SeqRows ws{};
-      AttnItem now;  // the item to load: the one before the last announced
-      now.rows = 0;
-      int ids_now = -1;
-#pragma unroll 1
-      for (; live && left > 0 && b < B; ++b) {
-        if (win < 0 || b >= win + 32) {
-          win = b;
-          ws = SeqRows{};
-          if (b + lane < B) seq_rows(p.rows, c.kv_len, cap, b + lane, ws);
-        }
-        AttnItem it;
-        it.b = b;
-        it.L = __shfl_sync(0xffffffffu, ws.L, b - win);
-        it.n = __shfl_sync(0xffffffffu, ws.n, b - win);
-        it.first = __shfl_sync(0xffffffffu, ws.first, b - win);
-        const int R = it.n * G, count = item_count(R);
-        if (count == 0) continue;
-        int h = 0;
-        if (!located) {
-          located = true;
-          const long long hu = head_units(p, it.L, it.n, G);
-          h = static_cast<int>(off / hu);
-          off -= h * hu;
-        }
-#pragma unroll 1
-        for (int x = h * count; live && left > 0 && x < Hk * count; ++x) {
-          it.h = x / count;
-          it.row0 = (x - it.h * count) * kAtItemRows;
-          it.rows = min(kAtItemRows, R - it.row0);
-          const ItemRange rg = item_range(p, it.L, it.n, it.row0, it.rows);
-          const int nt = tile_count(rg), u = max(1, nt);
-          if (off >= u) {  // (only while the first item is being located)
-            off -= u;
-            continue;
+    // The dealer's state: the sequence, its rows and items per head, the next item among its heads,
+    // the units to skip before the first item and those left of this CTA's run.
+    int b = u0 < u1 ? *s_start - 1 : B, R = 0, count = 0, x = 0, loads = 0, fixes = 0;
+    long long off = *s_off, left = u1 - u0;
+    int win = -64;  // the lanes hold the rows of 32 sequences
+    SeqRows ws{}, sq{};
+    // the next item of the run (rows == 0: the end)
+    auto deal = [&](AttnItem& it) {
+      it.rows = 0;
+      while (left > 0) {
+        if (x >= Hk * count) {  // the next sequence with rows
+          if (++b >= B) return;
+          if (b >= win + 32) {
+            win = b;
+            ws = SeqRows{};
+            if (b + lane < B) seq_rows(p.rows, c.kv_len, cap, b + lane, ws);
           }
-          const int o = static_cast<int>(off);
-          const int take = static_cast<int>(min(static_cast<long long>(u - o), left));
-          off = 0;
-          left -= take;
-          it.t0 = first_tile(rg) + o;
-          it.nt = nt > 0 ? take : 0;
-          it.slot = o == 0 && take == u ? -1 : 2 * static_cast<int>(blockIdx.x) + (o == 0);
-          it.load0 = loads;
-          it.lo = rg.lo;
-          it.hi = rg.hi;
-          it.full0 = (rg.flo + kAtTile - 1) / kAtTile;
-          it.full1 = max(it.full0, rg.fhi / kAtTile);
-          it.fix0 = fixes;
-          loads += 2 * it.nt;
-          fixes += it.partials_before(it.t0 + it.nt);
-          if (lane == 0 && o == 0 && take < u)
-            p.join[blockIdx.x] = AttnJoin{b, it.h, it.row0, it.rows, it.first,
-                                          1 + static_cast<int>((u - take + quota - 1) / quota)};
-          live = announce(it);
-          const int ids = fetch_ids(it, first_window(it));
-          if (live && now.rows > 0) live = load_item(now, ids_now);
-          now = it;
-          ids_now = ids;
+          sq.L = __shfl_sync(0xffffffffu, ws.L, b - win);
+          sq.n = __shfl_sync(0xffffffffu, ws.n, b - win);
+          sq.first = __shfl_sync(0xffffffffu, ws.first, b - win);
+          R = sq.n * G;
+          count = item_count(R);
+          x = 0;
+          if (off > 0 && count > 0) {  // (only the first sequence)
+            const long long hu = head_units(p, sq.L, sq.n, G);
+            x = static_cast<int>(off / hu) * count;
+            off %= hu;
+          }
+          continue;
         }
+        const int h = x / count, row0 = (x - h * count) * kAtItemRows;
+        ++x;
+        const int rows = min(kAtItemRows, R - row0);
+        const ItemRange rg = item_range(p, sq.L, sq.n, row0, rows);
+        const int nt = tile_count(rg), u = max(1, nt);
+        if (off >= u) {  // (only while the first item is being located)
+          off -= u;
+          continue;
+        }
+        const int o = static_cast<int>(off);
+        const int take = static_cast<int>(min(static_cast<long long>(u - o), left));
+        off = 0;
+        left -= take;
+        it.b = b;
+        it.h = h;
+        it.row0 = row0;
+        it.rows = rows;
+        it.L = sq.L;
+        it.n = sq.n;
+        it.first = sq.first;
+        it.t0 = first_tile(rg) + o;
+        it.nt = nt > 0 ? take : 0;
+        it.slot = o == 0 && take == u ? -1 : 2 * static_cast<int>(blockIdx.x) + (o == 0);
+        it.load0 = loads;
+        it.lo = rg.lo;
+        it.hi = rg.hi;
+        it.full0 = (rg.flo + kAtTile - 1) / kAtTile;
+        it.full1 = max(it.full0, rg.fhi / kAtTile);
+        it.fix0 = fixes;
+        loads += 2 * it.nt;
+        fixes += it.partials_before(it.t0 + it.nt);
+        if (lane == 0 && o == 0 && take < u)
+          p.join[blockIdx.x] = AttnJoin{b, h, row0, rows, sq.first,
+                                        1 + static_cast<int>((u - take + quota - 1) / quota)};
+        return;
       }
-      if (live) {
-        AttnItem end{};
-        live = announce(end);
+    };
+    auto announce = [&](const AttnItem& it) {
+      const int d = items % kAtDescs;
+      if (!wait(kBarItemFree + d, (items / kAtDescs) ^ 1)) return false;
+      if (lane == 0) {
+        s_items[d] = it;
+        mbar_arrive(bar(kBarItem + d));
       }
-      if (live && now.rows > 0) load_item(now, ids_now);
-    } else {
-      AttnItem now, it;
-      now.rows = 0;
-      int ids_now = -1;
-      while (live && fetch(it)) {
-        const int ids = it.rows > 0 ? fetch_ids(it, first_window(it)) : -1;
-        if (now.rows > 0) live = load_item(now, ids_now);
-        if (it.rows == 0) break;
-        now = it;
-        ids_now = ids;
+      ++items;
+      return true;
+    };
+    AttnItem now, it;
+    now.rows = 0;
+    int ids_now = -1;
+    while (true) {
+      if (is_k) {
+        deal(it);
+        live = announce(it);
+      } else {
+        live = fetch(it);
       }
+      if (!live) break;
+      const int ids = it.rows > 0 ? fetch_ids(it, first_window(it)) : -1;
+      if (now.rows > 0) live = load_item(now, ids_now);
+      if (!live || it.rows == 0) break;
+      now = it;
+      ids_now = ids;
     }
     if (*s_abort && last >= 0)  // let the copies in flight land
       drain_wait(bar(kBarFull + lane), (last / kStages) & 1);
