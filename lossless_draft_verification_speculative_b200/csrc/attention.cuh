@@ -186,6 +186,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
 #undef DSPARK_IN
 }
 #undef DSPARK_R32
+// 16 bytes from global to shared memory; the last 16 - bytes of them are zeros.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
 // mbar_wait with little code (it is inlined often, and the kernel's code should stay in the
 // instruction cache): an expired wait sets the abort flag, which the CTA counts once at its end.
 __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
@@ -766,17 +772,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const int rows = my_rows(a), row0 = my_row0(a);
       uint8_t* dst = sm + Sm::kQ + s * Sm::kStage;
       const T* q = static_cast<const T*>(p.q.p);
-      const int ch = r % kCh;
+      const int ch = r % kCh, bytes = 8 * ch < D ? 16 : 0;
 #pragma unroll 4
       for (int row = r / kCh; row < rows; row += kAtTile / kCh) {
-        const int i = p.by_group.div(row0 + row), head = a.h * G + row0 + row - i * G;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (8 * ch < D)
-          v = *reinterpret_cast<const uint4*>(q + token_offset(p.q, p, a.b, a.first, i) +
-                                              head * p.q.head_stride + 8 * ch);
-        *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kAtTile * 128) + row * 128 +
-                                  (((ch & 7) ^ (row & 7)) << 4)) = v;
+        const int i = p.by_group.div(row0 + row), h = a.h * G + row0 + row - i * G;
+        const T* src = q + token_offset(p.q, p, a.b, a.first, i) + h * p.q.head_stride +
+                       (bytes ? 8 * ch : 0);
+        copy16_async(smem_u32(dst) + (ch >> 3) * (kAtTile * 128) + row * 128 +
+                         (((ch & 7) ^ (row & 7)) << 4),
+                     src, bytes);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarQ + s));
@@ -918,10 +924,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, z + 32 * q);
           tmem_ld_wait();
           if (partial) {
-            const int a = lo - x0, e = hi - x0;
+            // the row's seen positions as bits, 32 at a time
 #pragma unroll
-            for (int q = 0; q < kAtTile; ++q)
-              if (q < a || q >= e) z[q] = -INFINITY;
+            for (int y = 0; y < 4; ++y) {
+              const int a = min(max(lo - x0 - 32 * y, 0), 32), e = min(max(hi - x0 - 32 * y, 0), 32);
+              const uint32_t seen = static_cast<uint32_t>((1ull << e) - (1ull << min(a, e)));
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (!((seen >> q) & 1)) z[32 * y + q] = -INFINITY;
+            }
           }
           float mx[4];
 #pragma unroll
