@@ -204,12 +204,6 @@ __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile 
   return false;
 }
 
-// max of three; a NaN loses against a number.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -936,13 +930,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           float mx[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) mx[y] = max3(z[2 * y], z[2 * y + 1], -INFINITY);
+          for (int y = 0; y < 4; ++y) mx[y] = max_nan(z[2 * y], z[2 * y + 1]);
 #pragma unroll
           for (int q = 8; q < kAtTile; q += 8) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], z[q + 2 * y], z[q + 2 * y + 1]);
+            for (int y = 0; y < 4; ++y) mx[y] = max3_nan(mx[y], z[q + 2 * y], z[q + 2 * y + 1]);
           }
-          const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          const float mt = max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]);
+          if (!(mt < INFINITY)) poison = true;  // a NaN or an infinity among the seen scores
           // the kept maximum moves when the tile's exceeds it by kAtRescale binary orders
           const bool move = real && mt > m && !((mt - m) * cl <= kAtRescale);
           if (__any_sync(0xffffffffu, move)) {
