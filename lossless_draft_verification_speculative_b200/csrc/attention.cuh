@@ -128,6 +128,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
+// A value known to be the same in every lane, as such.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 // D = A B (first) or D += A B, both operands in shared memory.
 __device__ __forceinline__ void at_mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                           uint32_t idesc, uint32_t accumulate) {
@@ -669,23 +671,25 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         auto qk = [&](int s, int j) {
           // (a descriptor's start address counts 16 bytes: a step of 16 dims is 2, the next 64
           // dims a tile's half on)
-          const uint64_t q0 = sw128_desc(sb + Sm::kQ + s * Sm::kStage);
+          const uint32_t t_s = uniform(tbase + s * 128);
+          const uint64_t q0 = sw128_desc(uniform(sb + Sm::kQ + s * Sm::kStage));
           const uint64_t k0 =
-              sw128_desc(sb + Sm::kKv + stage(load_of_k(j, look)) * Sm::kStage);
+              sw128_desc(uniform(sb + Sm::kKv + stage(load_of_k(j, look)) * Sm::kStage));
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k) {
             const int at = (k >> 2) * (kAtTile * 8) + 2 * (k & 3);
-            if (16 * k < D) at_mma_ss(tbase + s * 128, q0 + at, k0 + at, qk_desc, k != 0);
+            at_mma_ss(t_s, q0 + at, k0 + at, qk_desc, k != 0);
           }
           at_commit(bar(kBarS + s));
         };
         // O_s += P_s V_j
         auto pv = [&](int s, int j, bool first) {
+          const uint32_t t_o = uniform(tbase + 256 + s * 128), t_p = uniform(tbase + s * 128);
           const uint64_t v0 =
-              sw128_mn_desc(sb + Sm::kKv + stage(load_of_v(j, look, nt)) * Sm::kStage);
+              sw128_mn_desc(uniform(sb + Sm::kKv + stage(load_of_v(j, look, nt)) * Sm::kStage));
 #pragma unroll
           for (int k = 0; k < kAtTile / 16; ++k)
-            at_mma_ts(tbase + 256 + s * 128, tbase + s * 128 + 8 * k,
+            at_mma_ts(t_o, t_p + 8 * k,
                        v0 + 128 * k, pv_desc, !(first && k == 0));
         };
         auto free_stage = [&](int idx) { at_commit(bar(kBarEmpty + stage(idx))); };
