@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional, Tuple, Union
 
 import torch
@@ -70,82 +71,90 @@ def _lib() -> ctypes.CDLL:
     return lib
 
 
+# The structs above are filled through `struct` (a tenth of the cost of their constructors: the
+# calls on a few tokens are short).
+_HEADS, _ROWS, _CACHE = struct.Struct("@Qqqq"), struct.Struct("@iiQQ"), struct.Struct("@QQ6q4iQqiQ")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _int32(t: torch.Tensor, n: int, name: str, device) -> None:
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != device or \
+def _int32(t: torch.Tensor, n: int, name: str, device) -> int:
+    if t.dtype is not torch.int32 or t.shape != (n,) or t.device != device or \
             (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on q's device")
+    return t.data_ptr()
 
 
 def _check_rows(q: torch.Tensor, kv_len: torch.Tensor, n_new: Optional[torch.Tensor],
-                q_start: Optional[torch.Tensor]) -> Rows:
+                q_start: Optional[torch.Tensor]) -> Tuple[int, int, int, int]:
+    """The fields of Rows."""
     if not q.is_cuda:
         raise RuntimeError("the cache-side calls run on CUDA tensors only")
     if q.dtype not in CACHE_DTYPES:
         raise ValueError("q must be bfloat16 or float16")
+    dev = q.device
     B = kv_len.shape[0] if kv_len.dim() == 1 else -1
-    _int32(kv_len, B, "kv_len", q.device)
     if q_start is not None:
         if n_new is not None:
             raise ValueError("n_new belongs to a block of rows, q_start to packed ones")
         if q.dim() != 3:
             raise ValueError("with q_start, q must be [T, heads, head_dim]")
-        _int32(q_start, B + 1, "q_start", q.device)
-        return Rows(B, q.shape[0], None, q_start.data_ptr())
+        return B, q.shape[0], 0, _int32(q_start, B + 1, "q_start", dev)
     if q.dim() != 4 or q.shape[0] != B:
         raise ValueError("q must be [B, N, heads, head_dim] (or packed, with q_start)")
-    if n_new is not None:
-        _int32(n_new, B, "n_new", q.device)
-    return Rows(B, q.shape[1], _ptr(n_new), None)
+    return B, q.shape[1], 0 if n_new is None else _int32(n_new, B, "n_new", dev), 0
 
 
 def _heads(t: torch.Tensor, like: torch.Tensor, heads: int, name: str) -> Heads:
     """The head-row tensor t: the rows and element type of `like`, `heads` heads."""
-    if t.dtype != like.dtype or t.device != like.device or t.dim() != like.dim() or \
-            t.shape[:-2] != like.shape[:-2] or t.shape[-2] != heads or \
-            t.shape[-1] != like.shape[-1] or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    shape, stride = t.shape, t.stride()
+    if t is not like and (t.dtype is not like.dtype or t.device != like.device or
+                          len(shape) != like.dim() or shape[:-2] != like.shape[:-2] or
+                          shape[-2] != heads or shape[-1] != like.shape[-1]) or \
+            (shape[-1] > 1 and stride[-1] != 1):
         raise ValueError(f"{name} must have {heads} heads of q's rows, head_dim, dtype and "
                          "device, its last dimension contiguous")
-    s = t.stride()
-    return Heads(t.data_ptr(), s[0] if len(s) == 4 else 0, s[-3], s[-2])
+    return Heads.from_buffer_copy(_HEADS.pack(
+        t.data_ptr(), stride[0] if len(stride) == 4 else 0, stride[-3], stride[-2]))
 
 
 def _check_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
                  kv_len: torch.Tensor, q: torch.Tensor) -> KvCache:
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != q.shape[-1]:
+    shape, dev, dtype = k_pages.shape, q.device, q.dtype
+    if len(shape) != 4 or shape != v_pages.shape or shape[3] != q.shape[-1]:
         raise ValueError("k_pages and v_pages must be [pages, page_size, heads, head_dim] with "
                          "q's head_dim")
-    if k_pages.dtype != q.dtype or v_pages.dtype != q.dtype or k_pages.device != q.device or \
-            v_pages.device != q.device:
+    if k_pages.dtype is not dtype or v_pages.dtype is not dtype or k_pages.device != dev or \
+            v_pages.device != dev:
         raise ValueError("k_pages and v_pages must have q's dtype and device")
     ks, vs = k_pages.stride(), v_pages.stride()
-    if k_pages.shape[3] > 1 and (ks[3] != 1 or vs[3] != 1):
+    if shape[3] > 1 and (ks[3] != 1 or vs[3] != 1):
         raise ValueError("the last dimension of the pages must be contiguous")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or \
-            page_table.shape[0] != kv_len.shape[0] or page_table.device != q.device or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    kv_ptr = _int32(kv_len, kv_len.shape[0] if kv_len.dim() == 1 else -1, "kv_len", dev)
+    ts = page_table.shape
+    if page_table.dtype is not torch.int32 or len(ts) != 2 or ts[0] != kv_len.shape[0] or \
+            page_table.device != dev or (ts[1] > 1 and page_table.stride(1) != 1):
         raise ValueError("page_table must be an int32 [B, max_pages] tensor on q's device with "
                          "contiguous rows")
-    n_pages, ps, heads, D = k_pages.shape
-    cols = page_table.shape[1]
     # (a table of one row has no row stride to speak of)
-    ld = page_table.stride(0) if page_table.shape[0] > 1 else cols
-    return KvCache(k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1],
-                   vs[2], n_pages, ps, heads, D, page_table.data_ptr(), ld, cols,
-                   kv_len.data_ptr())
+    ld = page_table.stride(0) if ts[0] > 1 else ts[1]
+    return KvCache.from_buffer_copy(_CACHE.pack(
+        k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+        *shape, page_table.data_ptr(), ld, ts[1], kv_ptr))
 
 
 def _run(device, fn, what: str, *args) -> None:
     """Call the library on the tensors' device and its current stream."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream)
+            rc = fn(*args, _raw_stream(index))
     if rc != DSPARK_OK:
         raise DsparkError(rc, what)
 
@@ -207,13 +216,14 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: to
         if R > q.shape[-1]:
             raise ValueError("inv_freq rotates more elements than a head has")
     if status is not None:
-        _int32(status, rows.B, "status", dev)
+        _int32(status, rows[0], "status", dev)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     Hq, Hk = q.shape[-2], k_pages.shape[2]
     _run(dev, lib.dspark_rotary_append, "dspark_rotary_append", _heads(q, q, Hq, "q"), Hq,
          _heads(out, q, Hq, "out"), _heads(k, q, Hk, "k"), _heads(v, q, Hk, "v"),
-         CACHE_DTYPES[q.dtype], cache, rows, _ptr(inv_freq), R, int(interleaved),
+         CACHE_DTYPES[q.dtype], cache, Rows.from_buffer_copy(_ROWS.pack(*rows)),
+         None if inv_freq is None else inv_freq.data_ptr(), R, int(interleaved),
          float(magnitude), _ptr(status))
     return out
 
@@ -252,16 +262,17 @@ def block_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                             lse.device != dev or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor of q's shape without head_dim")
     if status is not None:
-        _int32(status, rows.B, "status", dev)
+        _int32(status, rows[0], "status", dev)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if workspace is None:
-        nbytes = lib.dspark_block_attention_workspace_bytes(rows.N, Hq, Hk, D)
+        nbytes = lib.dspark_block_attention_workspace_bytes(rows[1], Hq, Hk, D)
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
     _run(dev, lib.dspark_block_attention, "dspark_block_attention", _heads(q, q, Hq, "q"), Hq,
-         _heads(out, q, Hq, "out"), CACHE_DTYPES[q.dtype], cache, rows,
+         _heads(out, q, Hq, "out"), CACHE_DTYPES[q.dtype], cache,
+         Rows.from_buffer_copy(_ROWS.pack(*rows)),
          1.0 / math.sqrt(D) if scale is None else float(scale), int(causal),
          0 if window is None else min(int(window), 0x7fffffff), _ptr(lse), _ptr(status), workspace.data_ptr(),
          workspace.numel() * workspace.element_size())

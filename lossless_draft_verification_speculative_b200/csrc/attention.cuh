@@ -290,7 +290,7 @@ struct AttnSmem {
   static constexpr int kBad = kItems + kAtDescs * 64;         // [kAtBadRing][4] masks
   static constexpr int kNf = kBad + kAtBadRing * 16;          // [kAtFixRing][4] masks
   static constexpr int kMl = kNf + kAtFixRing * 16;                       // [128] float2
-  static constexpr int kMisc = kMl + 1024;                    // tmem base, abort, start, scan
+  static constexpr int kMisc = kMl + 1024;                    // tensor memory's base, abort flag
   static constexpr int kTotal = kMisc + 128;
 };
 static_assert(sizeof(AttnItem) == 64, "item descriptor");
@@ -337,9 +337,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   uint32_t* s_nf = reinterpret_cast<uint32_t*>(sm + Sm::kNf);
   float2* s_ml = reinterpret_cast<float2*>(sm + Sm::kMl);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + Sm::kMisc);
-  int* s_start = reinterpret_cast<int*>(sm + Sm::kMisc + 8);                 // sequence
-  long long* s_off = reinterpret_cast<long long*>(sm + Sm::kMisc + 16);      // unit within it
-  long long* s_scan = reinterpret_cast<long long*>(sm + Sm::kMisc + 24);     // [12]
 
   const int tid = threadIdx.x, wi = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const dspark_kv_cache_t& c = p.cache;
@@ -351,60 +348,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     for (int i = 0; i < kBarCount; ++i)
       mbar_init(bar(i), i < kBarP ? 1 : i < kBarItemFree ? 4 : 11);
     *s_abort = 0;
-    *s_start = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
   if (wi == 9) tmem_alloc_all(s_tmem);
-  grid_dependency_wait();  // lengths, queries and the cache come from the kernels before
-  grid_dependents_launch();
-
-  // ---- this CTA's run of units: a scan of the sequences' units, a few sequences per thread
-  const int B = p.rows.B, per = (B + kAtThreads - 1) / kAtThreads;
-  const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) {
-    SeqRows s;
-    if (seq_rows(p.rows, c.kv_len, cap, b, s)) mine += Hk * head_units(p, s.L, s.n, G);
-  }
-  long long upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) s_scan[wi] = upto;
-  __syncthreads();
-  long long total = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < kAtThreads / 32; ++w) {
-    if (w < wi) before += s_scan[w];
-    total += s_scan[w];
-  }
-  upto += before;
-  const long long quota = (total + gridDim.x - 1) / gridDim.x;
-  const long long u0 = quota * blockIdx.x;
-  const long long u1 = min(total, u0 + quota);
-  if (u0 < u1 && u0 >= upto - mine && u0 < upto) {
-    long long off = u0 - (upto - mine);
-    for (int b = b_lo; b < b_hi; ++b) {
-      SeqRows s;
-      if (!seq_rows(p.rows, c.kv_len, cap, b, s)) continue;
-      const long long u = Hk * head_units(p, s.L, s.n, G);
-      if (off < u) {
-        *s_start = b;
-        *s_off = off;
-        break;
-      }
-      off -= u;
-    }
-  }
-  if (tid == 0) p.join[blockIdx.x].pieces = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = __shfl_sync(0xffffffffu, *s_tmem, 0);
+  grid_dependency_wait();  // lengths, queries and the cache come from the kernels before
+  grid_dependents_launch();
 
   // the next announced item (rows == 0: the end); false on an abort
   int items = 0;
@@ -498,10 +452,39 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
     // The dealer's state: the sequence, its rows and items per head, the next item among its heads,
     // the units to skip before the first item and those left of this CTA's run.
-    int b = u0 < u1 ? *s_start - 1 : B, R = 0, count = 0, x = 0, loads = 0, fixes = 0;
-    long long off = *s_off, left = u1 - u0;
+    const int B = p.rows.B;
+    int b = B, R = 0, count = 0, x = 0, loads = 0, fixes = 0;
+    long long off = 0, left = 0, quota = 1;
     int win = -64;  // the lanes hold the rows of 32 sequences
     SeqRows ws{}, sq{};
+    if (is_k) {
+      // this CTA's run: a scan of the sequences' units, `per` neighbouring sequences a lane
+      const int per = (B + 31) / 32, b_lo = min(B, lane * per), b_hi = min(B, b_lo + per);
+      long long mine = 0;
+#pragma unroll 4
+      for (int i = b_lo; i < b_hi; ++i) {
+        seq_rows(p.rows, c.kv_len, cap, i, ws);
+        mine += Hk * head_units(p, ws.L, ws.n, G);
+      }
+      if (per == 1) win = 0;  // (one sequence a lane: ws holds it)
+      long long upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const long long total = __shfl_sync(0xffffffffu, upto, 31);
+      // two units a CTA at least: the two softmax groups take one each, in the time of one
+      quota = max(2ll, (total + gridDim.x - 1) / gridDim.x);
+      const long long u0 = quota * blockIdx.x;
+      left = min(quota, total - u0);
+      if (left > 0) {
+        const int at = __popc(__ballot_sync(0xffffffffu, upto <= u0));  // the lane of unit u0
+        off = u0 - __shfl_sync(0xffffffffu, upto - mine, at);
+        b = at * per - 1;  // (the walk steps to the next sequence first)
+      }
+      if (lane == 0) p.join[blockIdx.x].pieces = 0;
+    }
     // the next item of the run (rows == 0: the end)
     auto deal = [&](AttnItem& it) {
       it.rows = 0;
@@ -519,10 +502,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           R = sq.n * G;
           count = item_count(R);
           x = 0;
-          if (off > 0 && count > 0) {  // (only the first sequence)
+          if (off > 0 && count > 0) {  // (only until the first item is located)
             const long long hu = head_units(p, sq.L, sq.n, G);
-            x = static_cast<int>(off / hu) * count;
-            off %= hu;
+            x = static_cast<int>(min(off / hu, static_cast<long long>(Hk))) * count;
+            off -= x / count * hu;
           }
           continue;
         }
