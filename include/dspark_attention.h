@@ -46,7 +46,7 @@ typedef struct {
  *    tokens, 0 <= n_new[b] <= N (n_new == NULL: N everywhere), its first rows.
  *  Packed (q_start != NULL): tensors are [N, heads, head_dim]; sequence b has the rows
  *    q_start[b] .. q_start[b+1] - 1, 0 <= q_start[b] <= q_start[b+1] <= N. n_new must be NULL.
- * Rows that belong to no sequence are never read, and never written. */
+ * Rows that belong to no sequence have no effect and are never written. */
 typedef struct {
   int B, N;
   const int32_t* n_new;   /* device [B] or NULL */

@@ -70,8 +70,9 @@ cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, size_t smem, cudaStr
 template <typename T>
 dspark_status_t rotary_launch(RotaryParams p, bool vec, cudaStream_t stream) {
   const int total = p.rows.q_start ? p.rows.N : p.rows.B * p.rows.N;
-  // several tokens a CTA once every SM has enough CTAs: the angles are then one pass of the CTA
-  p.tokens = total >= 8 * kPlanSMs * kRotMaxTokens ? kRotMaxTokens : 1;
+  // 2 or 4 tokens a CTA while every SM still has at least 8 CTAs
+  p.tokens = 1;
+  while (p.tokens < kRotMaxTokens && total >= 8 * kPlanSMs * 2 * p.tokens) p.tokens *= 2;
   int slots = (p.cache.head_dim + 15) / 16;
   p.log_slots = 0;
   while ((1 << p.log_slots) < slots) ++p.log_slots;
@@ -79,7 +80,8 @@ dspark_status_t rotary_launch(RotaryParams p, bool vec, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       dependent_launch(dim3(static_cast<unsigned>(ctas > 0 ? ctas : 1)), kRotThreads,
-                       static_cast<size_t>(p.tokens) * (p.R / 2) * sizeof(float2), stream, attr);
+                       (static_cast<size_t>(p.tokens) * (p.R / 2) + 8) * sizeof(float2), stream,
+                       attr);  // (8: the last slot of interleaved pairs may read past its own)
   const cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, rotary_append_kernel<T, true>, p)
                             : cudaLaunchKernelEx(&cfg, rotary_append_kernel<T, false>, p);
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;

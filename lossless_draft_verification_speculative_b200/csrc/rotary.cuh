@@ -84,7 +84,7 @@ struct Half16<__half> {
 // ---------------------------------------------------------------------------- the kernel
 
 constexpr int kRotThreads = 256;
-constexpr int kRotMaxTokens = 4;  // tokens per CTA
+constexpr int kRotMaxTokens = 4;  // tokens per CTA, at most (a warp finds each)
 
 struct RotaryParams {
   dspark_heads_t q, q_out, k, v;
@@ -185,27 +185,20 @@ __device__ __forceinline__ void rotary_status(const RotaryParams& p) {
 // One CTA: p.tokens rows, every head. Vector path (kVec): every row start is 16-byte aligned
 // and the pairs fall into whole 8-element vectors. A head is cut into slots of two vectors:
 // the two halves of eight (i, i + R/2) pairs, or two neighbouring vectors (interleaved pairs,
-// the copied rest, v); the thread keeps its slot, and its eight cos/sin, over a token's heads.
+// the copied rest, v). A thread keeps its slot and takes every (256 / slots)-th (token, head); its
+// first one is loaded before the lengths, pages and angles are known, so that both latencies
+// overlap. Memory bound: 10205 tokens of 32 + 8 + 8 heads of 128 (251 MB) take 47 to 49 us, 5.2 TB/s,
+// 81% of the measured copy rate. Several loads in flight a thread cost more in registers (resident
+// warps) than they bring: 2, 4 and 6 took 51.2, 54.4 and 70.6 us; 2 or 8 tokens a CTA 48.8 and
+// above 50 us.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const RotaryParams p) {
-  extern __shared__ float2 s_cs[];
+  extern __shared__ __align__(16) float2 s_cs[];
   __shared__ RotaryToken s_tok[kRotMaxTokens];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int total = p.rows.q_start ? p.rows.N : p.rows.B * p.rows.N;
   const int row0 = blockIdx.x * p.tokens;
   const int nt = min(p.tokens, total - row0);
-
-  grid_dependency_wait();  // lengths, values and the cache come from the kernels before
-  grid_dependents_launch();
-  if (warp < nt) {
-    const RotaryToken t = rotary_token(p, row0 + warp, lane);
-    if (lane == 0) s_tok[warp] = t;
-  }
-  __syncthreads();
-  rotary_angles(p, s_tok, nt, s_cs);
-  if (p.status) rotary_status(p);
-  __syncthreads();
-
   const int Hk = p.cache.n_heads, H = p.Hq + 2 * Hk, D = p.cache.head_dim, R = p.R;
   const T* q = static_cast<const T*>(p.q.p);
   const T* k = static_cast<const T*>(p.k.p);
@@ -213,108 +206,130 @@ __global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const Rotary
   T* qo = static_cast<T*>(p.q_out.p);
   T* kp = static_cast<T*>(p.cache.k);
   T* vp = static_cast<T*>(p.cache.v);
-  for (int t = 0; t < nt; ++t) {
-    const RotaryToken tok = s_tok[t];
-    if (tok.pos < 0) continue;
-    const float2* cs = s_cs + t * (R / 2);
-    const int64_t q_at = row_offset(p.q, p.rows, tok.row);
-    const int64_t o_at = row_offset(p.q_out, p.rows, tok.row);
-    const int64_t k_at = row_offset(p.k, p.rows, tok.row);
-    const int64_t v_at = row_offset(p.v, p.rows, tok.row);
-    // the source and destination of head h (q, then k, then v); false: nothing to write
-    auto rows_of = [&](int h, const T*& src, T*& dst) {
-      if (h < p.Hq) {
-        src = q + q_at + h * p.q.head_stride;
-        dst = qo + o_at + h * p.q_out.head_stride;
-        return true;
-      }
-      h -= p.Hq;
-      if (h < Hk) {
-        src = k + k_at + h * p.k.head_stride;
-        dst = kp + tok.k_at + h * p.cache.k_head_stride;
-        return tok.k_at >= 0;
-      }
-      h -= Hk;
-      src = v + v_at + h * p.v.head_stride;
-      dst = vp + tok.v_at + h * p.cache.v_head_stride;
-      return tok.v_at >= 0;
-    };
-    if (kVec) {
-      const int slot = tid & ((1 << p.log_slots) - 1);
-      const int nvec = D / 8, rvec = R / 8;
-      if (2 * slot >= nvec) continue;
-      const bool split = !p.interleaved && slot < rvec / 2;  // a pair slot of the half layout
-      const int va = split ? slot : 2 * slot, vb = split ? slot + rvec / 2 : 2 * slot + 1;
-      const bool has_b = vb < nvec;
-      float2 w[8];
-      const int pair0 = 8 * slot;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pair0 + i < R / 2 ? cs[pair0 + i] : make_float2(1.f, 0.f);
-      const int stride = kRotThreads >> p.log_slots;
-#pragma unroll 2
-      for (int h = tid >> p.log_slots; h < H; h += stride) {
-        const T* src;
-        T* dst;
-        if (!rows_of(h, src, dst)) continue;
-        const bool is_v = h >= p.Hq + Hk;
-        const int a0 = is_v ? 2 * slot : va, b0 = is_v ? 2 * slot + 1 : vb;
-        const bool hb = is_v ? 2 * slot + 1 < nvec : has_b;
-        uint4 x = *reinterpret_cast<const uint4*>(src + 8 * a0);
-        uint4 y = hb ? *reinterpret_cast<const uint4*>(src + 8 * b0) : make_uint4(0, 0, 0, 0);
+  // head h of a token counts q's heads, then k's, then v's
+  auto source = [&](int t, int h) {
+    if (h < p.Hq) return q + row_offset(p.q, p.rows, row0 + t) + h * p.q.head_stride;
+    h -= p.Hq;
+    if (h < Hk) return k + row_offset(p.k, p.rows, row0 + t) + h * p.k.head_stride;
+    return v + row_offset(p.v, p.rows, row0 + t) + (h - Hk) * p.v.head_stride;
+  };
+  // null: nothing to write
+  auto target = [&](const RotaryToken& tok, int h) -> T* {
+    if (tok.pos < 0) return nullptr;
+    if (h < p.Hq) return qo + row_offset(p.q_out, p.rows, tok.row) + h * p.q_out.head_stride;
+    h -= p.Hq;
+    if (h < Hk) return tok.k_at < 0 ? nullptr : kp + tok.k_at + h * p.cache.k_head_stride;
+    return tok.v_at < 0 ? nullptr : vp + tok.v_at + (h - Hk) * p.cache.v_head_stride;
+  };
+
+  const int slot = tid & ((1 << p.log_slots) - 1), stride = kRotThreads >> p.log_slots;
+  const int nvec = D / 8, rvec = R / 8;
+  const bool split = !p.interleaved && slot < rvec / 2;  // a pair slot of the half layout
+  const bool idle = 2 * slot >= nvec;
+  int t = 0, h = tid >> p.log_slots;  // this thread's (token, head)
+  while (h >= H) {
+    h -= H;
+    ++t;
+  }
+  // the slot's two vectors in head h
+  auto vectors = [&](int h, int& a, int& b) {
+    const bool pairs = split && h < p.Hq + Hk;
+    a = pairs ? slot : 2 * slot;
+    b = pairs ? slot + rvec / 2 : 2 * slot + 1;
+  };
+  uint4 x, y;
+  auto load_slot = [&](int t, int h) {
+    int a, b;
+    vectors(h, a, b);
+    const T* src = source(t, h);
+    x = *reinterpret_cast<const uint4*>(src + 8 * a);
+    if (b < nvec) y = *reinterpret_cast<const uint4*>(src + 8 * b);
+  };
+
+  grid_dependency_wait();  // lengths, values and the cache come from the kernels before
+  grid_dependents_launch();
+  if (kVec && !idle && t < nt) load_slot(t, h);
+  if (warp < nt) {
+    const RotaryToken tok = rotary_token(p, row0 + warp, lane);
+    if (lane == 0) s_tok[warp] = tok;
+  }
+  __syncthreads();
+  rotary_angles(p, s_tok, nt, s_cs);
+  if (p.status) rotary_status(p);
+  __syncthreads();
+
+  if (kVec) {
+    if (idle) return;
+    while (t < nt) {
+      if (T* dst = target(s_tok[t], h)) {
+        int a, b;
+        vectors(h, a, b);
         uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
         uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
-        if (!is_v) {
+        const bool turn = h < p.Hq + Hk && (split || (p.interleaved && a < rvec));
+        if (turn) {
+          float2 w[8];
+          const float4* cs = reinterpret_cast<const float4*>(s_cs + t * (R / 2) + 8 * slot);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 c = cs[j];
+            w[2 * j] = make_float2(c.x, c.y);
+            w[2 * j + 1] = make_float2(c.z, c.w);
+          }
           if (p.interleaved) {
             // words of x are pairs 0..3 of the slot, words of y pairs 4..7
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (a0 < rvec) {
-                const float2 f = Half16<T>::up(xw[i]);
-                xw[i] = Half16<T>::down(f.x * w[i].x - f.y * w[i].y, f.y * w[i].x + f.x * w[i].y);
-              }
-              if (b0 < rvec) {
-                const float2 f = Half16<T>::up(yw[i]);
-                yw[i] = Half16<T>::down(f.x * w[4 + i].x - f.y * w[4 + i].y,
-                                        f.y * w[4 + i].x + f.x * w[4 + i].y);
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = Half16<T>::up(xw[j]);
+              xw[j] = Half16<T>::down(f.x * w[j].x - f.y * w[j].y, f.y * w[j].x + f.x * w[j].y);
+              if (b < rvec) {
+                const float2 g = Half16<T>::up(yw[j]), z = w[4 + j];
+                yw[j] = Half16<T>::down(g.x * z.x - g.y * z.y, g.y * z.x + g.x * z.y);
               }
             }
-          } else if (split) {
+          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = Half16<T>::up(xw[i]), g = Half16<T>::up(yw[i]);
-              const float2 c0 = w[2 * i], c1 = w[2 * i + 1];
-              xw[i] = Half16<T>::down(f.x * c0.x - g.x * c0.y, f.y * c1.x - g.y * c1.y);
-              yw[i] = Half16<T>::down(g.x * c0.x + f.x * c0.y, g.y * c1.x + f.y * c1.y);
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = Half16<T>::up(xw[j]), g = Half16<T>::up(yw[j]);
+              const float2 c0 = w[2 * j], c1 = w[2 * j + 1];
+              xw[j] = Half16<T>::down(f.x * c0.x - g.x * c0.y, f.y * c1.x - g.y * c1.y);
+              yw[j] = Half16<T>::down(g.x * c0.x + f.x * c0.y, g.y * c1.x + f.y * c1.y);
             }
           }
         }
-        *reinterpret_cast<uint4*>(dst + 8 * a0) = x;
-        if (hb) *reinterpret_cast<uint4*>(dst + 8 * b0) = y;
+        *reinterpret_cast<uint4*>(dst + 8 * a) = x;
+        if (b < nvec) *reinterpret_cast<uint4*>(dst + 8 * b) = y;
       }
-    } else {
-      // element path: a thread per pair, then per copied element
-      const int half = R / 2, units = half + (D - R);
-      for (int j = tid; j < H * units; j += kRotThreads) {
-        const int h = j / units, u = j - h * units;
-        const T* src;
-        T* dst;
-        if (!rows_of(h, src, dst)) continue;
-        if (u >= half) {
-          const int d = R + (u - half);
-          dst[d] = src[d];
-          continue;
-        }
-        const int d1 = p.interleaved ? 2 * u : u, d2 = p.interleaved ? 2 * u + 1 : u + half;
-        const T x1 = src[d1], x2 = src[d2];
-        if (h >= p.Hq + Hk) {
-          dst[d1] = x1;
-          dst[d2] = x2;
-        } else {
-          const float a = Half16<T>::up1(x1), b = Half16<T>::up1(x2);
-          const float2 w = cs[u];
-          dst[d1] = Half16<T>::down1(a * w.x - b * w.y);
-          dst[d2] = Half16<T>::down1(b * w.x + a * w.y);
-        }
+      h += stride;
+      while (h >= H) {
+        h -= H;
+        ++t;
+      }
+      if (t < nt) load_slot(t, h);
+    }
+  } else {
+    // element path: a thread per pair, then per copied element
+    const int half = R / 2, units = half + (D - R);
+    for (int j = tid; j < nt * H * units; j += kRotThreads) {
+      const int row = j / units, u = j - row * units, ti = row / H, hi = row - ti * H;
+      T* dst = target(s_tok[ti], hi);
+      if (!dst) continue;
+      const T* src = source(ti, hi);
+      if (u >= half) {
+        const int d = R + (u - half);
+        dst[d] = src[d];
+        continue;
+      }
+      const int d1 = p.interleaved ? 2 * u : u, d2 = p.interleaved ? 2 * u + 1 : u + half;
+      const T x1 = src[d1], x2 = src[d2];
+      if (hi >= p.Hq + Hk) {
+        dst[d1] = x1;
+        dst[d2] = x2;
+      } else {
+        const float f = Half16<T>::up1(x1), g = Half16<T>::up1(x2);
+        const float2 w = s_cs[ti * half + u];
+        dst[d1] = Half16<T>::down1(f * w.x - g * w.y);
+        dst[d2] = Half16<T>::down1(g * w.x + f * w.y);
       }
     }
   }
