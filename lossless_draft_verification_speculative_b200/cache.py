@@ -74,6 +74,7 @@ def _lib() -> ctypes.CDLL:
 # The structs above are filled through `struct` (a tenth of the cost of their constructors: the
 # calls on a few tokens are short).
 _HEADS, _ROWS, _CACHE = struct.Struct("@Qqqq"), struct.Struct("@iiQQ"), struct.Struct("@QQ6q4iQqiQ")
+_pack_heads, _heads_of = _HEADS.pack, Heads.from_buffer_copy
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -109,17 +110,15 @@ def _check_rows(q: torch.Tensor, kv_len: torch.Tensor, n_new: Optional[torch.Ten
     return B, q.shape[1], 0 if n_new is None else _int32(n_new, B, "n_new", dev), 0
 
 
-def _heads(t: torch.Tensor, like: torch.Tensor, heads: int, name: str) -> Heads:
-    """The head-row tensor t: the rows and element type of `like`, `heads` heads."""
-    shape, stride = t.shape, t.stride()
-    if t is not like and (t.dtype is not like.dtype or t.device != like.device or
-                          len(shape) != like.dim() or shape[:-2] != like.shape[:-2] or
-                          shape[-2] != heads or shape[-1] != like.shape[-1]) or \
-            (shape[-1] > 1 and stride[-1] != 1):
-        raise ValueError(f"{name} must have {heads} heads of q's rows, head_dim, dtype and "
-                         "device, its last dimension contiguous")
-    return Heads.from_buffer_copy(_HEADS.pack(
-        t.data_ptr(), stride[0] if len(stride) == 4 else 0, stride[-3], stride[-2]))
+def _heads(t: torch.Tensor, shape: torch.Size, like: torch.Tensor, name: str) -> Heads:
+    """The head-row tensor t, of the given shape and of the element type and device of `like`."""
+    stride = t.stride()
+    if t.shape != shape or (shape[-1] > 1 and stride[-1] != 1) or \
+            (t is not like and (t.dtype is not like.dtype or t.device != like.device)):
+        raise ValueError(f"{name} must be {list(shape)} of q's dtype and device, its last "
+                         "dimension contiguous")
+    return _heads_of(_pack_heads(t.data_ptr(), stride[0] if len(stride) == 4 else 0, stride[-3],
+                                 stride[-2]))
 
 
 def _check_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
@@ -219,9 +218,11 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: to
         _int32(status, rows[0], "status", dev)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    Hq, Hk = q.shape[-2], k_pages.shape[2]
-    _run(dev, lib.dspark_rotary_append, "dspark_rotary_append", _heads(q, q, Hq, "q"), Hq,
-         _heads(out, q, Hq, "out"), _heads(k, q, Hk, "k"), _heads(v, q, Hk, "v"),
+    shape, Hk = q.shape, k_pages.shape[2]
+    kv_shape = torch.Size((*shape[:-2], Hk, shape[-1]))
+    _run(dev, lib.dspark_rotary_append, "dspark_rotary_append", _heads(q, shape, q, "q"),
+         shape[-2], _heads(out, shape, q, "out"), _heads(k, kv_shape, q, "k"),
+         _heads(v, kv_shape, q, "v"),
          CACHE_DTYPES[q.dtype], cache, Rows.from_buffer_copy(_ROWS.pack(*rows)),
          None if inv_freq is None else inv_freq.data_ptr(), R, int(interleaved),
          float(magnitude), _ptr(status))
@@ -270,8 +271,8 @@ def block_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
-    _run(dev, lib.dspark_block_attention, "dspark_block_attention", _heads(q, q, Hq, "q"), Hq,
-         _heads(out, q, Hq, "out"), CACHE_DTYPES[q.dtype], cache,
+    _run(dev, lib.dspark_block_attention, "dspark_block_attention", _heads(q, q.shape, q, "q"), Hq,
+         _heads(out, q.shape, q, "out"), CACHE_DTYPES[q.dtype], cache,
          Rows.from_buffer_copy(_ROWS.pack(*rows)),
          1.0 / math.sqrt(D) if scale is None else float(scale), int(causal),
          0 if window is None else min(int(window), 0x7fffffff), _ptr(lse), _ptr(status), workspace.data_ptr(),
