@@ -148,6 +148,16 @@ dspark_status_t dspark_block_attention(dspark_heads_t q, int n_q_heads, dspark_h
                                        float* lse, int32_t* status, void* workspace,
                                        size_t workspace_bytes, void* stream);
 
+/* For tests of the timeout path only: dspark_block_attention with each CTA's first copy of keys
+ * withheld, so that the waits for it run out (about a second) and the kernel gives up: the call
+ * returns DSPARK_OK, its outputs are incomplete and dspark_pipeline_timeouts grows. */
+dspark_status_t dspark_block_attention_withheld(dspark_heads_t q, int n_q_heads,
+                                                dspark_heads_t out, dspark_dtype_t dtype,
+                                                dspark_kv_cache_t cache, dspark_rows_t rows,
+                                                float scale, int causal, int window, float* lse,
+                                                int32_t* status, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -17,7 +17,7 @@ from __future__ import annotations
 import ctypes
 import math
 import struct
-from typing import Optional, Tuple, Union
+from typing import Optional, Tuple
 
 import torch
 
@@ -67,6 +67,8 @@ def _lib() -> ctypes.CDLL:
     lib.dspark_block_attention.restype = i32
     lib.dspark_block_attention.argtypes = [Heads, i32, Heads, i32, KvCache, Rows, f32, i32, i32,
                                            vp, vp, vp, sz, vp]
+    lib.dspark_block_attention_withheld.restype = i32
+    lib.dspark_block_attention_withheld.argtypes = lib.dspark_block_attention.argtypes
     lib._cache_side = True
     return lib
 
@@ -239,7 +241,8 @@ def block_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                     scale: Optional[float] = None, causal: bool = True,
                     window: Optional[int] = None, out: Optional[torch.Tensor] = None,
                     lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
-                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+                    workspace: Optional[torch.Tensor] = None,
+                    _withhold: bool = False) -> torch.Tensor:
     """Attention of the new tokens over the paged cache, which already holds their keys.
 
     ``q`` (a block or packed rows, see the module) is already rotated; query head h reads cache
@@ -271,10 +274,18 @@ def block_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
-    _run(dev, lib.dspark_block_attention, "dspark_block_attention", _heads(q, q.shape, q, "q"), Hq,
+    fn = lib.dspark_block_attention_withheld if _withhold else lib.dspark_block_attention
+    _run(dev, fn, "dspark_block_attention", _heads(q, q.shape, q, "q"), Hq,
          _heads(out, q.shape, q, "out"), CACHE_DTYPES[q.dtype], cache,
          Rows.from_buffer_copy(_ROWS.pack(*rows)),
          1.0 / math.sqrt(D) if scale is None else float(scale), int(causal),
          0 if window is None else min(int(window), 0x7fffffff), _ptr(lse), _ptr(status), workspace.data_ptr(),
          workspace.numel() * workspace.element_size())
     return out
+
+
+def block_attention_withheld(*args, **kwargs) -> torch.Tensor:
+    """block_attention with the first copy of keys of every CTA withheld, for tests of the timeout
+    path only: its waits run out (about a second), the kernel gives up, ``pipeline_timeouts()``
+    grows and the result is incomplete."""
+    return block_attention(*args, _withhold=True, **kwargs)

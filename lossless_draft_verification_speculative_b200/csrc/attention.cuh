@@ -34,6 +34,10 @@
 //    from tensor memory). Q_s, written by the group, stays in shared memory for the item.
 // Tensor memory: S_0, S_1 (128 columns each, P_s over S_s), O_0, O_1 (128 columns each).
 //
+// Waits. Every mbarrier wait is bounded (2^31 clocks, about a second); one that runs out sets an
+// abort flag that ends every role's loop, is counted (dspark_pipeline_timeouts), lets the copies
+// and products in flight finish (again bounded) and frees the tensor memory.
+//
 // Unseen places. Scores outside a row's range become -inf whatever they are. A weight of 0 times
 // a non-finite value would be NaN, so in a tile that some row of the item does not see in full
 // the values outside the item's range, and any with a non-finite element, are zeroed in shared
@@ -75,6 +79,7 @@ struct AttnParams {
   int box, box_log2; // slots per TMA box: min(page_size, 128)
   int page_log2;
   int part_rows;     // rows of a partial result's slot
+  int withhold;      // (tests of the timeout path) each CTA's first K copy is not issued
   float* part_o;     // [2 CTAs][part_rows][DP]
   float2* part_ml;   // [2 CTAs][part_rows]: (c m, l)
   struct AttnJoin* join;  // [CTAs]
@@ -422,6 +427,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           s_bad[((it.load0 / 2 + j) % kAtBadRing) * 4 + lane] = m;
         }
         if (!wait(kBarEmpty + st, (g / kStages) ^ 1)) return false;
+        if (p.withhold && g == 0 && is_k) continue;
         if (lane == 0)
           mbar_arrive_tx(bar(kBarFull + st),
                          static_cast<uint32_t>(__popc(all)) * p.box * 128 * kHalves);

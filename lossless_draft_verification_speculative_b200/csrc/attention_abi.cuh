@@ -164,6 +164,59 @@ dspark_status_t attention_launch(AttnParams p, dspark_dtype_t dtype, const AttnW
              : DSPARK_ERR_CUDA;
 }
 
+dspark_status_t block_attention_impl(dspark_heads_t q, int n_q_heads, dspark_heads_t out,
+                                     dspark_dtype_t dtype, dspark_kv_cache_t cache,
+                                     dspark_rows_t rows, float scale, int causal, int window,
+                                     float* lse, int32_t* status, void* workspace,
+                                     size_t workspace_bytes, void* stream, int withhold) {
+  const dspark_status_t st = check_cache_call(cache, rows, n_q_heads, dtype, 128);
+  if (st != DSPARK_OK) return st;
+  if (!(scale > 0.f) || !std::isfinite(scale) || window < 0 || n_q_heads % cache.n_heads != 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (rows.B == 0) return DSPARK_OK;
+  const int D = cache.head_dim;
+  if (rows.N > 0 &&
+      (!heads_ok(q, rows, n_q_heads, D, false) || !heads_ok(out, rows, n_q_heads, D, true)))
+    return DSPARK_ERR_INVALID_ARG;
+  if (D < 16 || D % 8 != 0 || cache.page_size < 8 || cache.page_size > 1024 ||
+      (cache.page_size & (cache.page_size - 1)) != 0)
+    return DSPARK_ERR_UNSUPPORTED;
+  if (!heads_vec(q, rows, n_q_heads) || !heads_vec(out, rows, n_q_heads) || !cache_vec(cache) ||
+      !aligned(lse, 4))
+    return DSPARK_ERR_UNSUPPORTED;
+  const AttnWs ws = attention_ws(rows.N, n_q_heads, cache.n_heads, D);
+  if (!workspace || workspace_bytes < ws.total || !aligned(workspace, 256))
+    return DSPARK_ERR_WORKSPACE;
+  AttnParams p{};
+  p.q = q;
+  p.out = out;
+  p.cache = cache;
+  p.rows = rows;
+  p.lse = lse;
+  p.status = status;
+  p.Hq = n_q_heads;
+  p.by_group = fast_div(static_cast<uint32_t>(n_q_heads / cache.n_heads));
+  p.causal = causal != 0;
+  p.window = window;
+  p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  if (!std::isfinite(p.scale_log2)) return DSPARK_ERR_INVALID_ARG;
+  p.box = cache.page_size < kAtTile ? cache.page_size : kAtTile;
+  p.box_log2 = log2_of(p.box);
+  p.page_log2 = log2_of(cache.page_size);
+  char* w = static_cast<char*>(workspace);
+  p.part_rows = ws.part_rows;
+  p.withhold = withhold;
+  p.join = reinterpret_cast<AttnJoin*>(w + ws.join);
+  p.part_ml = reinterpret_cast<float2*>(w + ws.ml);
+  p.part_o = reinterpret_cast<float*>(w + ws.o);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == DSPARK_BF16)
+    return D <= 64 ? attention_launch<__nv_bfloat16, 64>(p, dtype, ws, s)
+                   : attention_launch<__nv_bfloat16, 128>(p, dtype, ws, s);
+  return D <= 64 ? attention_launch<__half, 64>(p, dtype, ws, s)
+                 : attention_launch<__half, 128>(p, dtype, ws, s);
+}
+
 }  // namespace
 }  // namespace dspark
 
@@ -262,50 +315,18 @@ dspark_status_t dspark_block_attention(dspark_heads_t q, int n_q_heads, dspark_h
                                        dspark_rows_t rows, float scale, int causal, int window,
                                        float* lse, int32_t* status, void* workspace,
                                        size_t workspace_bytes, void* stream) {
-  const dspark_status_t st = check_cache_call(cache, rows, n_q_heads, dtype, 128);
-  if (st != DSPARK_OK) return st;
-  if (!(scale > 0.f) || !std::isfinite(scale) || window < 0 || n_q_heads % cache.n_heads != 0)
-    return DSPARK_ERR_INVALID_ARG;
-  if (rows.B == 0) return DSPARK_OK;
-  const int D = cache.head_dim;
-  if (rows.N > 0 && (!heads_ok(q, rows, n_q_heads, D, false) || !heads_ok(out, rows, n_q_heads, D, true)))
-    return DSPARK_ERR_INVALID_ARG;
-  if (D < 16 || D % 8 != 0 || cache.page_size < 8 || cache.page_size > 1024 ||
-      (cache.page_size & (cache.page_size - 1)) != 0)
-    return DSPARK_ERR_UNSUPPORTED;
-  if (!heads_vec(q, rows, n_q_heads) || !heads_vec(out, rows, n_q_heads) || !cache_vec(cache) ||
-      !aligned(lse, 4))
-    return DSPARK_ERR_UNSUPPORTED;
-  const AttnWs ws = attention_ws(rows.N, n_q_heads, cache.n_heads, D);
-  if (!workspace || workspace_bytes < ws.total || !aligned(workspace, 256))
-    return DSPARK_ERR_WORKSPACE;
-  AttnParams p{};
-  p.q = q;
-  p.out = out;
-  p.cache = cache;
-  p.rows = rows;
-  p.lse = lse;
-  p.status = status;
-  p.Hq = n_q_heads;
-  p.by_group = fast_div(static_cast<uint32_t>(n_q_heads / cache.n_heads));
-  p.causal = causal != 0;
-  p.window = window;
-  p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
-  if (!std::isfinite(p.scale_log2)) return DSPARK_ERR_INVALID_ARG;
-  p.box = cache.page_size < kAtTile ? cache.page_size : kAtTile;
-  p.box_log2 = log2_of(p.box);
-  p.page_log2 = log2_of(cache.page_size);
-  char* w = static_cast<char*>(workspace);
-  p.part_rows = ws.part_rows;
-  p.join = reinterpret_cast<AttnJoin*>(w + ws.join);
-  p.part_ml = reinterpret_cast<float2*>(w + ws.ml);
-  p.part_o = reinterpret_cast<float*>(w + ws.o);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == DSPARK_BF16)
-    return D <= 64 ? attention_launch<__nv_bfloat16, 64>(p, dtype, ws, s)
-                   : attention_launch<__nv_bfloat16, 128>(p, dtype, ws, s);
-  return D <= 64 ? attention_launch<__half, 64>(p, dtype, ws, s)
-                 : attention_launch<__half, 128>(p, dtype, ws, s);
+  return block_attention_impl(q, n_q_heads, out, dtype, cache, rows, scale, causal, window, lse,
+                              status, workspace, workspace_bytes, stream, 0);
+}
+
+dspark_status_t dspark_block_attention_withheld(dspark_heads_t q, int n_q_heads,
+                                                dspark_heads_t out, dspark_dtype_t dtype,
+                                                dspark_kv_cache_t cache, dspark_rows_t rows,
+                                                float scale, int causal, int window, float* lse,
+                                                int32_t* status, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
+  return block_attention_impl(q, n_q_heads, out, dtype, cache, rows, scale, causal, window, lse,
+                              status, workspace, workspace_bytes, stream, 1);
 }
 
 }  // extern "C"

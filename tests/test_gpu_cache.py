@@ -227,6 +227,21 @@ def test_two_calls_at_once():
         assert all(torch.equal(x, want[i]) for x in got[i])
 
 
+@pytest.mark.parametrize("n,D", [(4, 128), (200, 64)])
+def test_timeout_path(n, D):
+    """With every CTA's first copy of keys withheld the waits for it run out: the kernel gives up
+    and frees what it holds, the counter grows, and the next call is right."""
+    from lossless_draft_verification_speculative_b200.cache import block_attention_withheld
+
+    c = Paged([700], 1, D, 16, "bf16", seed=30)
+    q = queries([n], 4, D, "bf16")
+    before = dv.pipeline_timeouts()
+    block_attention_withheld(q[0][None].to(DEV), **c.device())
+    torch.cuda.synchronize()
+    assert dv.pipeline_timeouts() > before
+    check_attention(c, q, [n], "bf16")
+
+
 # --------------------------------------------------------------------------- rotary append
 
 def check_rotary(kv_len, n_new, Hq, Hk, D, R, ps, dtype, *, interleaved=False, packed=False,
