@@ -584,11 +584,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   } else if (wi == 11) {
     // ------------------------------------------------------------------ unseen values
     // In a tile that some row of the item does not see in full: the values outside the item's
-    // range, or with an element that is not finite, become zeros; the latter are noted.
+    // range become zeros, and so do those that only some rows see and that have an element that
+    // is not finite; the latter are noted.
     AttnItem it;
     bool live = true;
     while (live && fetch(it) && it.rows > 0) {
       const int look = look_ahead(it.rows, it.nt);
+      const ItemRange rg = item_range(p, it.L, it.n, it.row0, it.rows);
       int fix = it.fix0;
       for (int j = 0; j < it.nt && live; ++j) {
         if (!it.partial(it.t0 + j)) continue;
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           uint8_t* v = sm + Sm::kKv + (g % kStages) * Sm::kStage + r * 128;
           const bool outside = x < it.lo || x >= it.hi;
           uint32_t odd = 0;
-          if (!outside) {
+          if (!outside && (x < rg.flo || x >= rg.fhi)) {
 #pragma unroll
             for (int q = 0; q < DP / 8; ++q) {
               const uint4 e = *reinterpret_cast<const uint4*>(
