@@ -15,8 +15,9 @@
 //
 // Rows and items. The n G rows (new token, query head) of a sequence and cache head are cut into
 // items of at most 128 rows when there are so few, else 256: an item's rows all read the same
-// keys. A unit is a tile of 128 positions of one item. The call's units, in the order (sequence,
-// cache head, item, tile), are dealt in equal contiguous runs to one CTA per SM, so sequences
+// keys. A unit is a tile of 128 positions of one item (or the like of a tile's time, for an
+// item's own cost: without it 64 decode tokens over 256 to 4096 positions took 84 us instead of
+// 70). The call's units, in the order (sequence, cache head, item, tile), are dealt in equal contiguous runs to one CTA per SM, so sequences
 // of any lengths balance; an item that a run's border cuts is finished by
 // attention_join_kernel from float32 partial results (at most two per CTA).
 //
@@ -59,6 +60,7 @@ constexpr int kAtThreads = 384;    // three warpgroups: two of softmax, one of t
 constexpr int kAtGroupRegs = 216, kAtOtherRegs = 72;
 constexpr int kAtTile = 128;        // positions per tile (and rows per softmax group)
 constexpr int kAtItemRows = 256;    // rows of an item, at most
+constexpr int kAtItemUnits = 3;     // what an item costs beside its tiles, in tiles
 constexpr int kAtDescs = 4;         // items announced ahead
 constexpr int kAtBadRing = 16;      // tiles whose bad-page masks are kept
 constexpr int kAtFixRing = 8;       // tiles whose masks of zeroed values are kept
@@ -253,14 +255,15 @@ __device__ __forceinline__ int first_tile(const ItemRange& r) { return r.lo / kA
 __device__ __forceinline__ int tile_count(const ItemRange& r) {
   return r.hi > r.lo ? (r.hi + kAtTile - 1) / kAtTile - r.lo / kAtTile : 0;
 }
-// Units of one cache head of a sequence: its items' tiles, at least one per item.
+// Units of one cache head of a sequence: its items' tiles, and kAtItemUnits before each item's
+// first for what an item costs beside its tiles.
 __device__ __forceinline__ long long head_units(const AttnParams& p, int L, int n, int G) {
   const int R = n * G, items = item_count(R);
   long long u = 0;
 #pragma unroll 1
   for (int i = 0; i < items; ++i)
-    u += max(1, tile_count(item_range(p, L, n, i * kAtItemRows,
-                                      min(kAtItemRows, R - i * kAtItemRows))));
+    u += kAtItemUnits + tile_count(item_range(p, L, n, i * kAtItemRows,
+                                              min(kAtItemRows, R - i * kAtItemRows)));
   return u;
 }
 // Element offset of token i of sequence b.
@@ -519,15 +522,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         ++x;
         const int rows = min(kAtItemRows, R - row0);
         const ItemRange rg = item_range(p, sq.L, sq.n, row0, rows);
-        const int nt = tile_count(rg), u = max(1, nt);
+        const int nt = tile_count(rg), u = kAtItemUnits + nt;
         if (off >= u) {  // (only while the first item is being located)
           off -= u;
           continue;
         }
+        // this run's units of the item, and the tiles among them
         const int o = static_cast<int>(off);
         const int take = static_cast<int>(min(static_cast<long long>(u - o), left));
         off = 0;
         left -= take;
+        const int t_lo = max(0, o - kAtItemUnits), t_hi = max(0, o + take - kAtItemUnits);
+        if (nt > 0 ? t_hi <= t_lo : o > 0) continue;
         it.b = b;
         it.h = h;
         it.row0 = row0;
@@ -535,9 +541,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         it.L = sq.L;
         it.n = sq.n;
         it.first = sq.first;
-        it.t0 = first_tile(rg) + o;
-        it.nt = nt > 0 ? take : 0;
-        it.slot = o == 0 && take == u ? -1 : 2 * static_cast<int>(blockIdx.x) + (o == 0);
+        it.t0 = first_tile(rg) + t_lo;
+        it.nt = t_hi - t_lo;
+        it.slot = t_lo == 0 && t_hi == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (t_lo == 0);
         it.load0 = loads;
         it.lo = rg.lo;
         it.hi = rg.hi;
@@ -546,9 +552,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         it.fix0 = fixes;
         loads += 2 * it.nt;
         fixes += it.partials_before(it.t0 + it.nt);
-        if (lane == 0 && o == 0 && take < u)
+        if (lane == 0 && t_lo == 0 && t_hi < nt)
           p.join[blockIdx.x] = AttnJoin{b, h, row0, rows, sq.first,
-                                        1 + static_cast<int>((u - take + quota - 1) / quota)};
+                                        1 + static_cast<int>((nt - t_hi + quota - 1) / quota)};
         return;
       }
     };
