@@ -15,6 +15,7 @@ packed rows ``[T, heads, head_dim]`` with ``q_start`` (int32 ``[B+1]``), sequenc
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import struct
 from typing import Optional, Tuple
@@ -231,7 +232,10 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: to
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def block_attention_workspace_bytes(N: int, n_q_heads: int, n_heads: int, head_dim: int) -> int:
+    """Bytes of workspace that block_attention needs (N: the block's tokens per sequence, or
+    all packed ones); 0 for an unsupported shape."""
     return int(_lib().dspark_block_attention_workspace_bytes(N, n_q_heads, n_heads, head_dim))
 
 
@@ -270,7 +274,7 @@ def block_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if workspace is None:
-        nbytes = lib.dspark_block_attention_workspace_bytes(rows[1], Hq, Hk, D)
+        nbytes = block_attention_workspace_bytes(rows[1], Hq, Hk, D)
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")

@@ -102,6 +102,30 @@ def test_heads_first_storage_and_strided_rows():
         assert torch.equal(a[i, :n[i]], b[i, :n[i]])
 
 
+def test_layouts_of_keys_beside_values():
+    """Values before keys in memory, both in one tensor, and keys and values of different
+    strides give what two plain tensors give."""
+    n = [3, 5]
+    c = Paged([70, 200], 2, 64, 16, "bf16", seed=40)
+    q = torch.full((2, 5, 4, 64), 1.0, dtype=torch.bfloat16, device=DEV)
+    for b, x in enumerate(queries(n, 4, 64, "bf16")):
+        q[b, :n[b]] = x.to(DEV)
+    kw = dict(n_new=torch.tensor(n, dtype=torch.int32, device=DEV))
+    d = c.device()
+    want = dv.block_attention(q, **d, **kw, out=torch.zeros_like(q))
+    pair = torch.stack([d["v_pages"], d["k_pages"]])                     # values first
+    inner = torch.stack([d["k_pages"], d["v_pages"]], dim=1)             # page by page
+    mixed = d["v_pages"].transpose(1, 2).contiguous().transpose(1, 2)    # other strides
+    for k, v in ((pair[1], pair[0]), (inner[:, 0], inner[:, 1]), (d["k_pages"], mixed),
+                 (mixed, mixed)):
+        got = dv.block_attention(q, **{**d, "k_pages": k, "v_pages": v}, **kw,
+                                 out=torch.zeros_like(q))
+        if k is v:  # keys that are the values: another result, but a defined one
+            want = dv.block_attention(q, **{**d, "k_pages": d["v_pages"]}, **kw,
+                                      out=torch.zeros_like(q))
+        assert torch.equal(got, want)
+
+
 def test_scale_and_large_scores():
     """Peaked rows (scores of hundreds): the running maximum moves, nothing overflows."""
     n = [4]
