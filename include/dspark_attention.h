@@ -123,7 +123,7 @@ dspark_status_t dspark_rotary_append(dspark_heads_t q, int n_q_heads, dspark_hea
 
 /* Attention of the new tokens over the paged cache (their own keys and values appended).
  *  q, out    [.., n_q_heads, head_dim] of `dtype` (DSPARK_BF16 or DSPARK_F16, the cache's type
- *            too); query head h reads cache head h / (n_q_heads / n_heads).
+ *            too); query head h reads cache head h / (n_q_heads / n_heads). out may be q itself.
  *  New token i of sequence b, at position p = kv_len[b] - n + i, sees the positions t < kv_len[b]
  *  with t <= p when `causal`, and t > p - window when window > 0; out = sum_t w_t v_t with
  *  w = softmax over the seen t of scale * q . k_t. A token that sees nothing gives zeros (and
@@ -134,8 +134,9 @@ dspark_status_t dspark_rotary_append(dspark_heads_t q, int n_q_heads, dspark_hea
  *            log of the sum of exp(scale * q . k_t) over the seen t (natural logarithm).
  *  status    device [B] or NULL. A token that sees a position whose page id is out of range
  *            gives NaN (DSPARK_SEQ_BAD_PAGE); the others are not affected.
- *  Limits: head_dim a multiple of 8 in [16, 128]; page_size a power of two in [8, 1024];
- *  pointers and strides multiples of 16 bytes (else DSPARK_ERR_UNSUPPORTED).
+ *  Limits (else DSPARK_ERR_UNSUPPORTED): head_dim a multiple of 8 in [16, 128]; page_size a
+ *  power of two in [8, 1024]; at most 4096 heads and 65535 sequences; pointers and strides
+ *  multiples of 16 bytes, the cache's strides below 2^40 bytes.
  *  Numerics: scores and sums in float32 on the tensor cores; the weights are rounded to
  *  `dtype` for the product with v (a relative 2^-8 (bf16) or 2^-11 (f16) each at most), the
  *  statistics are not; out is rounded once.

@@ -44,7 +44,7 @@ dspark_status_t check_cache_call(const dspark_kv_cache_t& c, const dspark_rows_t
       (c.page_size > 1 && (c.k_token_stride < D || c.v_token_stride < D)) ||
       (c.n_heads > 1 && (c.k_head_stride < D || c.v_head_stride < D)))
     return DSPARK_ERR_INVALID_ARG;
-  if (c.head_dim > max_dim || Hq > 4096) return DSPARK_ERR_UNSUPPORTED;
+  if (c.head_dim > max_dim || Hq > 4096 || c.n_heads > 4096) return DSPARK_ERR_UNSUPPORTED;
   const long long rows = r.q_start ? r.N : static_cast<long long>(r.B) * r.N;
   if (rows * Hq > INT32_MAX || r.B > 65535 ||
       static_cast<long long>(c.max_pages) * c.page_size > (1 << 30))

@@ -75,9 +75,10 @@ def _attend(lib, **kw):
     (INV, dict(q=dict(p=None))), (INV, dict(out=dict(p=None))),
     (INV, dict(q=dict(token_stride=-8))),
     (INV, dict(out=dict(head_stride=0))), (INV, dict(out=dict(seq_stride=0))),
-    (UNS, dict(D=2048)), (UNS, dict(rows=dict(B=70000))),
+    (UNS, dict(D=2048)), (UNS, dict(Hq=8192, Hk=8192, ps=8)), (UNS, dict(rows=dict(B=70000))),
     (UNS, dict(rows=dict(B=60000, N=60000))),
     (UNS, dict(cache=dict(max_pages=1 << 28, ld_table=1 << 28))),
+    (UNS, dict(cache=dict(max_pages=(1 << 26) + 1, ld_table=1 << 27))),
     (OK, dict(rows=dict(B=0))),
 ])
 def test_shared_refusals(lib, call, want, kw):

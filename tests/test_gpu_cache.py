@@ -206,6 +206,18 @@ def test_bad_parameters_and_pages():
     assert torch.equal(out[:4], good[0]) and (out[4:] == 55.0).all()
 
 
+@pytest.mark.parametrize("n,L", [([4, 2], [900, 33]), ([300], [700])])
+def test_result_over_the_queries(n, L):
+    """out may be q itself, for whole items and for ones that several CTAs share."""
+    c = Paged(L, 2, 64, 16, "bf16", seed=41)
+    q = torch.cat(queries(n, 8, 64, "bf16")).to(DEV)
+    starts = torch.tensor([0] + list(np.cumsum(n)), dtype=torch.int32, device=DEV)
+    want = dv.block_attention(q, **c.device(), q_start=starts)
+    got = dv.block_attention(q, **c.device(), q_start=starts, out=q)
+    torch.cuda.synchronize()
+    assert got is q and torch.equal(got, want)
+
+
 def test_empty_calls():
     c = Paged([30], 1, 64, 16, "bf16")
     d = c.device()
