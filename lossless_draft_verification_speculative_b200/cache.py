@@ -16,7 +16,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import math
 import struct
 from typing import Optional, Tuple
 
@@ -78,46 +77,44 @@ def _lib() -> ctypes.CDLL:
 # calls on a few tokens are short).
 _HEADS, _ROWS, _CACHE = struct.Struct("@Qqqq"), struct.Struct("@iiQQ"), struct.Struct("@QQ6q4iQqiQ")
 _pack_heads, _heads_of = _HEADS.pack, Heads.from_buffer_copy
+_pack_rows, _rows_of = _ROWS.pack, Rows.from_buffer_copy
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
-def _int32(t: torch.Tensor, n: int, name: str, device) -> int:
-    if t.dtype is not torch.int32 or t.shape != (n,) or t.device != device or \
+def _int32(t: torch.Tensor, n: int, name: str, index: int) -> int:
+    if t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != index or \
             (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on q's device")
     return t.data_ptr()
 
 
 def _check_rows(q: torch.Tensor, kv_len: torch.Tensor, n_new: Optional[torch.Tensor],
-                q_start: Optional[torch.Tensor]) -> Tuple[int, int, int, int]:
-    """The fields of Rows."""
-    if not q.is_cuda:
+                q_start: Optional[torch.Tensor], index: int) -> Tuple[int, int, int, int]:
+    """The fields of Rows; `index` is q's device (-1: the CPU)."""
+    if index < 0:
         raise RuntimeError("the cache-side calls run on CUDA tensors only")
     if q.dtype not in CACHE_DTYPES:
         raise ValueError("q must be bfloat16 or float16")
-    dev = q.device
+    shape = q.shape
     B = kv_len.shape[0] if kv_len.dim() == 1 else -1
     if q_start is not None:
         if n_new is not None:
             raise ValueError("n_new belongs to a block of rows, q_start to packed ones")
-        if q.dim() != 3:
+        if len(shape) != 3:
             raise ValueError("with q_start, q must be [T, heads, head_dim]")
-        return B, q.shape[0], 0, _int32(q_start, B + 1, "q_start", dev)
-    if q.dim() != 4 or q.shape[0] != B:
+        return B, shape[0], 0, _int32(q_start, B + 1, "q_start", index)
+    if len(shape) != 4 or shape[0] != B:
         raise ValueError("q must be [B, N, heads, head_dim] (or packed, with q_start)")
-    return B, q.shape[1], 0 if n_new is None else _int32(n_new, B, "n_new", dev), 0
+    return B, shape[1], 0 if n_new is None else _int32(n_new, B, "n_new", index), 0
 
 
-def _heads(t: torch.Tensor, shape: torch.Size, like: torch.Tensor, name: str) -> Heads:
-    """The head-row tensor t, of the given shape and of the element type and device of `like`."""
+def _heads(t: torch.Tensor, shape: torch.Size, dtype: torch.dtype, index: int,
+           name: str) -> Heads:
+    """The head-row tensor t, of the given shape, element type and device."""
     stride = t.stride()
-    if t.shape != shape or (shape[-1] > 1 and stride[-1] != 1) or \
-            (t is not like and (t.dtype is not like.dtype or t.device != like.device)):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or \
+            (shape[-1] > 1 and stride[-1] != 1):
         raise ValueError(f"{name} must be {list(shape)} of q's dtype and device, its last "
                          "dimension contiguous")
     return _heads_of(_pack_heads(t.data_ptr(), stride[0] if len(stride) == 4 else 0, stride[-3],
@@ -125,37 +122,36 @@ def _heads(t: torch.Tensor, shape: torch.Size, like: torch.Tensor, name: str) ->
 
 
 def _check_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
-                 kv_len: torch.Tensor, q: torch.Tensor) -> KvCache:
-    shape, dev, dtype = k_pages.shape, q.device, q.dtype
-    if len(shape) != 4 or shape != v_pages.shape or shape[3] != q.shape[-1]:
+                 kv_len: torch.Tensor, head_dim: int, dtype: torch.dtype,
+                 index: int) -> KvCache:
+    shape, ks, vs = k_pages.shape, k_pages.stride(), v_pages.stride()
+    if len(shape) != 4 or shape != v_pages.shape or shape[3] != head_dim:
         raise ValueError("k_pages and v_pages must be [pages, page_size, heads, head_dim] with "
                          "q's head_dim")
-    if k_pages.dtype is not dtype or v_pages.dtype is not dtype or k_pages.device != dev or \
-            v_pages.device != dev:
+    if k_pages.dtype is not dtype or v_pages.dtype is not dtype or \
+            k_pages.get_device() != index or v_pages.get_device() != index:
         raise ValueError("k_pages and v_pages must have q's dtype and device")
-    ks, vs = k_pages.stride(), v_pages.stride()
     if shape[3] > 1 and (ks[3] != 1 or vs[3] != 1):
         raise ValueError("the last dimension of the pages must be contiguous")
-    kv_ptr = _int32(kv_len, kv_len.shape[0] if kv_len.dim() == 1 else -1, "kv_len", dev)
-    ts = page_table.shape
-    if page_table.dtype is not torch.int32 or len(ts) != 2 or ts[0] != kv_len.shape[0] or \
-            page_table.device != dev or (ts[1] > 1 and page_table.stride(1) != 1):
+    B = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    kv_ptr = _int32(kv_len, B, "kv_len", index)
+    ts, tstr = page_table.shape, page_table.stride()
+    if page_table.dtype is not torch.int32 or len(ts) != 2 or ts[0] != B or \
+            page_table.get_device() != index or (ts[1] > 1 and tstr[1] != 1):
         raise ValueError("page_table must be an int32 [B, max_pages] tensor on q's device with "
                          "contiguous rows")
     # (a table of one row has no row stride to speak of)
-    ld = page_table.stride(0) if ts[0] > 1 else ts[1]
     return KvCache.from_buffer_copy(_CACHE.pack(
         k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-        *shape, page_table.data_ptr(), ld, ts[1], kv_ptr))
+        *shape, page_table.data_ptr(), tstr[0] if B > 1 else ts[1], ts[1], kv_ptr))
 
 
-def _run(device, fn, what: str, *args) -> None:
+def _run(index: int, fn, what: str, *args) -> None:
     """Call the library on the tensors' device and its current stream."""
-    index = device.index
     if index == torch.cuda.current_device():
         rc = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, _raw_stream(index))
     if rc != DSPARK_OK:
         raise DsparkError(rc, what)
@@ -206,29 +202,26 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: to
     ``[B]``) receives SEQ_BAD_PARAM / SEQ_BAD_PAGE bits.
     """
     lib = _lib()
-    rows = _check_rows(q, kv_len, n_new, q_start)
-    cache = _check_cache(k_pages, v_pages, page_table, kv_len, q)
-    dev = q.device
-    R = 0
+    index, dtype, shape = q.get_device(), q.dtype, q.shape
+    rows = _check_rows(q, kv_len, n_new, q_start, index)
+    cache = _check_cache(k_pages, v_pages, page_table, kv_len, shape[-1], dtype, index)
+    R, freq = 0, None
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.device != dev or \
-                not inv_freq.is_contiguous():
+        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or \
+                inv_freq.get_device() != index or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous float32 vector on q's device")
-        R = 2 * inv_freq.shape[0]
-        if R > q.shape[-1]:
+        R, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+        if R > shape[-1]:
             raise ValueError("inv_freq rotates more elements than a head has")
-    if status is not None:
-        _int32(status, rows[0], "status", dev)
+    st = None if status is None else _int32(status, rows[0], "status", index)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    shape, Hk = q.shape, k_pages.shape[2]
-    kv_shape = torch.Size((*shape[:-2], Hk, shape[-1]))
-    _run(dev, lib.dspark_rotary_append, "dspark_rotary_append", _heads(q, shape, q, "q"),
-         shape[-2], _heads(out, shape, q, "out"), _heads(k, kv_shape, q, "k"),
-         _heads(v, kv_shape, q, "v"),
-         CACHE_DTYPES[q.dtype], cache, Rows.from_buffer_copy(_ROWS.pack(*rows)),
-         None if inv_freq is None else inv_freq.data_ptr(), R, int(interleaved),
-         float(magnitude), _ptr(status))
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    kv_shape = torch.Size((*shape[:-2], k_pages.shape[2], shape[-1]))
+    _run(index, lib.dspark_rotary_append, "dspark_rotary_append",
+         _heads(q, shape, dtype, index, "q"), shape[-2], _heads(out, shape, dtype, index, "out"),
+         _heads(k, kv_shape, dtype, index, "k"), _heads(v, kv_shape, dtype, index, "v"),
+         CACHE_DTYPES[dtype], cache, _rows_of(_pack_rows(*rows)), freq, R, int(interleaved),
+         float(magnitude), st)
     return out
 
 
@@ -260,30 +253,29 @@ def block_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     default one is taken from PyTorch's allocator for each call.
     """
     lib = _lib()
-    rows = _check_rows(q, kv_len, n_new, q_start)
-    cache = _check_cache(k_pages, v_pages, page_table, kv_len, q)
-    dev = q.device
-    Hq, Hk, D = q.shape[-2], k_pages.shape[2], q.shape[-1]
+    index, dtype, shape = q.get_device(), q.dtype, q.shape
+    rows = _check_rows(q, kv_len, n_new, q_start, index)
+    cache = _check_cache(k_pages, v_pages, page_table, kv_len, shape[-1], dtype, index)
+    Hq, D = shape[-2], shape[-1]
     if window is not None and window < 1:
         raise ValueError("window must be at least 1 (None: no window)")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:-1] or
-                            lse.device != dev or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:-1] or
+                            lse.get_device() != index or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor of q's shape without head_dim")
-    if status is not None:
-        _int32(status, rows[0], "status", dev)
+    st = None if status is None else _int32(status, rows[0], "status", index)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
     if workspace is None:
-        nbytes = block_attention_workspace_bytes(rows[1], Hq, Hk, D)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
+        nbytes = block_attention_workspace_bytes(rows[1], Hq, k_pages.shape[2], D)
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
     fn = lib.dspark_block_attention_withheld if _withhold else lib.dspark_block_attention
-    _run(dev, fn, "dspark_block_attention", _heads(q, q.shape, q, "q"), Hq,
-         _heads(out, q.shape, q, "out"), CACHE_DTYPES[q.dtype], cache,
-         Rows.from_buffer_copy(_ROWS.pack(*rows)),
-         1.0 / math.sqrt(D) if scale is None else float(scale), int(causal),
-         0 if window is None else min(int(window), 0x7fffffff), _ptr(lse), _ptr(status), workspace.data_ptr(),
+    _run(index, fn, "dspark_block_attention", _heads(q, shape, dtype, index, "q"), Hq,
+         _heads(out, shape, dtype, index, "out"), CACHE_DTYPES[dtype], cache,
+         _rows_of(_pack_rows(*rows)), D ** -0.5 if scale is None else float(scale), int(causal),
+         0 if window is None else min(int(window), 0x7fffffff),
+         None if lse is None else lse.data_ptr(), st, workspace.data_ptr(),
          workspace.numel() * workspace.element_size())
     return out
 

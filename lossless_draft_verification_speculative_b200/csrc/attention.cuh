@@ -81,6 +81,7 @@ struct AttnParams {
   int box, box_log2; // slots per TMA box: min(page_size, 128)
   int page_log2;
   int part_rows;     // rows of a partial result's slot
+  int which_k, which_v;  // last coordinate of keys and of values in their tensor maps
   int withhold;      // (tests of the timeout path) each CTA's first K copy is not issued
   float* part_o;     // [2 CTAs][part_rows][DP]
   float2* part_ml;   // [2 CTAs][part_rows]: (c m, l)
@@ -125,14 +126,14 @@ __device__ __forceinline__ void seen_range(int L, int n, int i, int causal, int 
 // The loader and the MMA issuer are whole warps that follow one path, so that addresses and
 // descriptors stay in uniform registers; one elected lane issues each of these instructions.
 // (Issued from inside a one-lane branch, eight products took 75 ns each instead of 34.)
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                            int z, int w, uint32_t bar) {
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, int w, int v, uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
-      "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      "@q cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
       : "memory");
 }
 // A value known to be the same in every lane, as such.
@@ -273,6 +274,11 @@ __device__ __forceinline__ int64_t token_offset(const dspark_heads_t& t, const A
                         : b * t.seq_stride + static_cast<int64_t>(i) * t.token_stride;
 }
 
+// a / b for non-negative values: a 32-bit division where both fit (it is on a call's critical path).
+__device__ __forceinline__ long long quick_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
 // Loads of an item of nt tiles, in ring order: the first `look` K tiles, then V_j and K_{j+look}
 // in turn. The index of K_j and of V_j among them.
 __device__ __forceinline__ int load_of_k(int j, int look) {
@@ -386,6 +392,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     // Warp 8 deals the items and loads K, warp 10 loads V.
     const bool is_k = wi == 8;
     const CUtensorMap* map = is_k ? &kmap : &vmap;
+    const int which = is_k ? p.which_k : p.which_v;
     const int boxes = kAtTile >> p.box_log2;
     bool live = true;
     int last = -1;  // lane i: the last load into stage i by this warp
@@ -450,7 +457,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if ((all >> (i0 + i)) & 1) {
 #pragma unroll
               for (int hf = 0; hf < kHalves; ++hf)
-                tma_load_4d(dst + hf * (kAtTile * 128), map, 64 * hf, y, it.h, pi[i],
+                tma_load_5d(dst + hf * (kAtTile * 128), map, 64 * hf, y, it.h, pi[i], which,
                             bar(kBarFull + st));
             }
           }
@@ -484,7 +491,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       }
       const long long total = __shfl_sync(0xffffffffu, upto, 31);
       // two units a CTA at least: the two softmax groups take one each, in the time of one
-      quota = max(2ll, (total + gridDim.x - 1) / gridDim.x);
+      quota = max(2ll, quick_div(total + gridDim.x - 1, gridDim.x));
       const long long u0 = quota * blockIdx.x;
       left = min(quota, total - u0);
       if (left > 0) {
@@ -513,7 +520,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           x = 0;
           if (off > 0 && count > 0) {  // (only until the first item is located)
             const long long hu = head_units(p, sq.L, sq.n, G);
-            x = static_cast<int>(min(off / hu, static_cast<long long>(Hk))) * count;
+            x = static_cast<int>(min(quick_div(off, hu), static_cast<long long>(Hk))) * count;
             off -= x / count * hu;
           }
           continue;
@@ -554,7 +561,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         fixes += it.partials_before(it.t0 + it.nt);
         if (lane == 0 && t_lo == 0 && t_hi < nt)
           p.join[blockIdx.x] = AttnJoin{b, h, row0, rows, sq.first,
-                                        1 + static_cast<int>((nt - t_hi + quota - 1) / quota)};
+                                        1 + static_cast<int>(quick_div(nt - t_hi + quota - 1, quota))};
         return;
       }
     };

@@ -153,20 +153,21 @@ def test_wrappers_need_cuda():
 def test_cache_layout_checks(over):
     t = _tensors(**over)
     with pytest.raises(ValueError):
-        ch._check_cache(t["k_pages"], t["v_pages"], t["page_table"], t["kv_len"], t["q"])
+        ch._check_cache(t["k_pages"], t["v_pages"], t["page_table"], t["kv_len"],
+                        t["q"].shape[-1], t["q"].dtype, -1)
 
 
 def test_head_layout_checks():
     q = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16)
     shape = torch.Size((2, 3, 2, 64))
-    ok = ch._heads(torch.zeros(2, 3, 6, 64, dtype=torch.bfloat16)[:, :, :2], shape, q, "k")
+    ok = ch._heads(torch.zeros(2, 3, 6, 64, dtype=torch.bfloat16)[:, :, :2], shape, q.dtype, -1, "k")
     assert (ok.seq_stride, ok.token_stride, ok.head_stride) == (3 * 6 * 64, 6 * 64, 64)
     for bad in (torch.zeros(2, 3, 2, 64), torch.zeros(2, 3, 3, 64, dtype=torch.bfloat16),
                 torch.zeros(2, 4, 2, 64, dtype=torch.bfloat16),
                 torch.zeros(6, 2, 64, dtype=torch.bfloat16),
                 torch.zeros(2, 3, 64, 2, dtype=torch.bfloat16).transpose(2, 3)):
         with pytest.raises(ValueError):
-            ch._heads(bad, shape, q, "k")
+            ch._heads(bad, shape, q.dtype, -1, "k")
 
 
 def test_struct_sizes_match_the_header():
