@@ -766,8 +766,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     auto my_row0 = [&](const AttnItem& a) {
       return a.row0 + (a.rows > kAtTile ? s * kAtTile : 0);
     };
-    // Q_s of an item into shared memory (128-byte swizzle, K-major); elements past head_dim zero,
-    // rows past the item's left as they are (their scores are never used)
+    // Q_s of an item into shared memory (128-byte swizzle, K-major); elements past head_dim and
+    // rows past the item's are zeros: their scores are never used, but the tensor cores' products
+    // of zeros draw less power, which sets the clock of a long run of calls
+    int q_rows = kAtTile;  // rows of Q_s that may hold something (at first whatever was there)
     auto load_q = [&](const AttnItem& a) {
       if (my_tiles(a, rel_next) == 0) return;
       constexpr int kCh = DP / 8;
@@ -784,6 +786,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                          (((ch & 7) ^ (row & 7)) << 4),
                      src, bytes);
       }
+      for (int row = rows + r / kCh; row < q_rows; row += kAtTile / kCh)
+        *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kAtTile * 128) + row * 128 +
+                                  ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+      q_rows = rows;
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
@@ -966,9 +972,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               }
             }
           }
-          const float base = m == -INFINITY ? 0.f : -m * cl;
-          // p = 2^(c z - c m), two at a time
-          const uint64_t c2 = pk2(cl, cl), base2 = pk2(base, base);
+          // p = 2^(c z - c m), two at a time; 0 in rows past the item's
+          const float base = !real ? -INFINITY : m == -INFINITY ? 0.f : -m * cl;
+          const float factor = real ? cl : 0.f;
+          const uint64_t c2 = pk2(factor, factor), base2 = pk2(base, base);
           uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int q = 0; q < kAtTile; q += 64) {
