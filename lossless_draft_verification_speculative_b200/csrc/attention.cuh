@@ -6,7 +6,10 @@
 // maximum m and sum l of the softmax: a tile of 128 positions adds p_t = 2^(c z_t - c m) to l and
 // p_t v_t to O (c = log2 e); when a new maximum exceeds m by more than 8 binary orders, l and O
 // are scaled by 2^(c m - c m'). Smaller excesses leave m as it is: p then reaches at most 2^8,
-// which costs float32 and the 16-bit weights no precision, and the rescaling of O is rare.
+// which costs float32 and the 16-bit weights no precision, and the rescaling of O is rare. f16
+// weights (and with them l and O) are made 2^7 times larger, up to 2^15: unscaled, the small
+// weights of a long context, each below 2^-25, would vanish while l counts them; now those below
+// 2^-32 do, 2^-12 of the result for 2^20 of them.
 //
 // What bounds it. The keys and values of a cache head are read once for all G query heads that
 // share it and all new tokens of the sequence: with few tokens 2 head_dim 2 bytes of HBM per
@@ -17,9 +20,10 @@
 // items of at most 128 rows when there are so few, else 256: an item's rows all read the same
 // keys. A unit is a tile of 128 positions of one item (or the like of a tile's time, for an
 // item's own cost: without it 64 decode tokens over 256 to 4096 positions took 84 us instead of
-// 70). The call's units, in the order (sequence, cache head, item, tile), are dealt in equal contiguous runs to one CTA per SM, so sequences
-// of any lengths balance; an item that a run's border cuts is finished by
-// attention_join_kernel from float32 partial results (at most two per CTA).
+// 70). The call's units, in the order (sequence, cache head, item, tile), are dealt in equal
+// contiguous runs to one CTA per SM, so sequences of any lengths balance; an item that a run's
+// border cuts is finished by attention_join_kernel from float32 partial results (at most two per
+// CTA).
 //
 // One CTA, 12 warps:
 //  - warps 0-3 and 4-7, softmax groups 0 and 1: thread = row = TMEM lane. Group s reads its scores
@@ -91,7 +95,7 @@ struct AttnParams {
   int which_k, which_v;  // last coordinate of keys and of values in their tensor maps
   int withhold;      // (tests of the timeout path) each CTA's first K copy is not issued
   float* part_o;     // [2 CTAs][part_rows][DP]
-  float2* part_ml;   // [2 CTAs][part_rows]: (c m, l)
+  float2* part_ml;   // [2 CTAs][part_rows]: (c m, less the weights' enlargement; l)
   struct AttnJoin* join;  // [CTAs]
 };
 
@@ -281,7 +285,7 @@ __device__ __forceinline__ int64_t token_offset(const dspark_heads_t& t, const A
                         : b * t.seq_stride + static_cast<int64_t>(i) * t.token_stride;
 }
 
-// a / b for non-negative values: a 32-bit division where both fit (it is on a call's critical path).
+// a / b for non-negative values: a 32-bit division where both fit (a call waits for it).
 __device__ __forceinline__ long long quick_div(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
@@ -342,6 +346,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                      const __grid_constant__ AttnParams p) {
   using Sm = AttnSmem<DP>;
   constexpr bool kBf = sizeof(T) == 2 && !std::is_same<T, __half>::value;
+  constexpr float kShift = kBf ? 0.f : 7.f;  // binary orders by which the weights are enlarged
   constexpr int kStages = Sm::kStages;
   constexpr int kHalves = DP / 64;
   extern __shared__ __align__(1024) uint8_t at_smem[];
@@ -567,8 +572,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         loads += 2 * it.nt;
         fixes += it.partials_before(it.t0 + it.nt);
         if (lane == 0 && t_lo == 0 && t_hi < nt)
-          p.join[blockIdx.x] = AttnJoin{b, h, row0, rows, sq.first,
-                                        1 + static_cast<int>(quick_div(nt - t_hi + quota - 1, quota))};
+          p.join[blockIdx.x] =
+              AttnJoin{b, h, row0, rows, sq.first,
+                       1 + static_cast<int>(quick_div(nt - t_hi + quota - 1, quota))};
         return;
       }
     };
@@ -889,10 +895,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           if (real) {
             if (it.slot >= 0)
-              p.part_ml[pr] = make_float2(m == -INFINITY ? m : m * cl, l);
+              p.part_ml[pr] = make_float2(m == -INFINITY ? m : m * cl - kShift, l);
             else if (p.lse)
               p.lse[static_cast<int64_t>(row) * p.Hq + head] =
-                  l == 0.f ? -INFINITY : (m * cl + log2f(l)) * 0.69314718055994531f;
+                  l == 0.f ? -INFINITY : (m * cl - kShift + log2f(l)) * 0.69314718055994531f;
           }
         }
         if (pair) {
@@ -942,7 +948,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             // the row's seen positions as bits, 32 at a time
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const int a = min(max(lo - x0 - 32 * y, 0), 32), e = min(max(hi - x0 - 32 * y, 0), 32);
+              const int at = x0 + 32 * y;
+              const int a = min(max(lo - at, 0), 32), e = min(max(hi - at, 0), 32);
               const uint32_t seen = static_cast<uint32_t>((1ull << e) - (1ull << min(a, e)));
 #pragma unroll
               for (int q = 0; q < 32; ++q)
@@ -980,7 +987,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
           }
           // p = 2^(c z - c m), two at a time; 0 in rows past the item's
-          const float base = !real ? -INFINITY : m == -INFINITY ? 0.f : -m * cl;
+          const float base = !real ? -INFINITY : m == -INFINITY ? 0.f : kShift - m * cl;
           const float factor = real ? cl : 0.f;
           const uint64_t c2 = pk2(factor, factor), base2 = pk2(base, base);
           uint64_t sum[4] = {0, 0, 0, 0};

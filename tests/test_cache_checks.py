@@ -160,7 +160,8 @@ def test_cache_layout_checks(over):
 def test_head_layout_checks():
     q = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16)
     shape = torch.Size((2, 3, 2, 64))
-    ok = ch._heads(torch.zeros(2, 3, 6, 64, dtype=torch.bfloat16)[:, :, :2], shape, q.dtype, -1, "k")
+    wide = torch.zeros(2, 3, 6, 64, dtype=torch.bfloat16)
+    ok = ch._heads(wide[:, :, :2], shape, q.dtype, -1, "k")
     assert (ok.seq_stride, ok.token_stride, ok.head_stride) == (3 * 6 * 64, 6 * 64, 64)
     for bad in (torch.zeros(2, 3, 2, 64), torch.zeros(2, 3, 3, 64, dtype=torch.bfloat16),
                 torch.zeros(2, 4, 2, 64, dtype=torch.bfloat16),

@@ -136,6 +136,20 @@ def test_scale_and_large_scores():
     check_attention(c, queries(n, 2, 64, "bf16"), n, "bf16", scale=1e-6)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("orders", [17.5, 25.5, 28.0])
+def test_many_small_weights(dtype, orders):
+    """One key stands out by many binary orders over 65535 equal ones, whose sum still counts."""
+    L, D = 65536, 16
+    c = Paged([L], 1, D, 256, dtype, seed=42)
+    c.k.zero_()
+    c.v.fill_(1.0)
+    c.k[c.table[0, 0].item(), 5, 0, 0] = 1.0
+    q = torch.zeros(1, 2, D, dtype=DT[dtype])
+    q[:, :, 0] = 8.0
+    check_attention(c, [q], [1], dtype, scale=orders * np.log(2.0) / 8.0)
+
+
 @pytest.mark.parametrize("n,Hq", [([8], 4), ([100, 8], 4)])
 def test_unseen_places_hold_anything(n, Hq):
     """Infinities and NaN in the cache where a token does not look (later tokens of its own
