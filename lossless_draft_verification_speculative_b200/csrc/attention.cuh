@@ -134,19 +134,20 @@ __device__ __forceinline__ void seen_range(int L, int n, int i, int causal, int 
 
 // ------------------------------------------------------------------------ PTX helpers
 
-// The loader and the MMA issuer are whole warps that follow one path, so that addresses and
-// descriptors stay in uniform registers; one elected lane issues each of these instructions.
-// (Issued from inside a one-lane branch, a 4096-token chunk at 12288 took 736 us instead of 609.)
+// One box of a tile: each lane of a loader issues its own. (One elected lane issuing them all: 374
+// us instead of 275 for the serving blocks in pages of 8, 367 instead of 295 for 128 of them with
+// heads of 64 in pages of 16; no difference from pages of 32 on.)
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             int z, int w, int v, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "@q cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(dst),
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
       : "memory");
 }
+// The MMA issuer is a whole warp that follows one path, so that addresses and descriptors stay in
+// uniform registers; one elected lane issues each product and commit. (Issued from inside a
+// one-lane branch, a 4096-token chunk at 12288 took 736 us instead of 609.)
 // A value known to be the same in every lane, as such.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 // D = A B (first) or D += A B, both operands in shared memory.
@@ -457,23 +458,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (!is_k && lane == 0 && it.partial(t))
           mbar_arrive(bar(kBarToFix + (it.fix0 + it.partials_before(t)) % kAtFixRing));
         __syncwarp();
-        uint32_t dst = sb + Sm::kKv + st * Sm::kStage;
-        const int y = p.box < kAtTile ? 0 : (t * kAtTile) & (c.page_size - 1);
-#pragma unroll 1
-        for (int i0 = 0; i0 < boxes; i0 += 4) {
-          int pi[4];
+        if (need) {
+          const uint32_t dst = sb + Sm::kKv + st * Sm::kStage + (lane << p.box_log2) * 128;
+          const int y = p.box < kAtTile ? 0 : (t * kAtTile) & (c.page_size - 1);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pi[i] = __shfl_sync(0xffffffffu, page, i0 + i);
-#pragma unroll
-          for (int i = 0; i < 4; ++i, dst += p.box * 128) {
-            if ((all >> (i0 + i)) & 1) {
-#pragma unroll
-              for (int hf = 0; hf < kHalves; ++hf)
-                tma_load_5d(dst + hf * (kAtTile * 128), map, 64 * hf, y, it.h, pi[i], which,
-                            bar(kBarFull + st));
-            }
-          }
+          for (int hf = 0; hf < kHalves; ++hf)
+            tma_load_5d(dst + hf * (kAtTile * 128), map, 64 * hf, y, it.h, page, which,
+                        bar(kBarFull + st));
         }
+        __syncwarp();
       }
       return true;
     };
