@@ -41,7 +41,7 @@
 //
 // Measured (one B200, back to back in a graph): blocks of up to 8 tokens of 64 sequences over 1024
 // to 16384 positions, 32 / 8 heads of 128, 1.47 GB: 233 us, 6.3 TB/s, 98% of the measured copy
-// rate. A 4096-token chunk at 12288: 574 us, 1.2 PFLOP/s, 73% of cuBLAS's bf16 rate in a burst; 664
+// rate. A 4096-token chunk at 12288: 574 us, 1.2 PFLOP/s, 73% of cuBLAS's bf16 rate in a burst; 667
 // us in seconds-long loops, where the power limit sets the clock (cuBLAS itself then makes 86% of
 // its burst rate). There a group's chain (scores, weights, both products) takes some 3600 clocks a
 // tile against 2048 of the tensor cores' own; a one-tile item costs 12 us beside its launch.
