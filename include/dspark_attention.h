@@ -46,7 +46,9 @@ typedef struct {
  *    tokens, 0 <= n_new[b] <= N (n_new == NULL: N everywhere), its first rows.
  *  Packed (q_start != NULL): tensors are [N, heads, head_dim]; sequence b has the rows
  *    q_start[b] .. q_start[b+1] - 1, 0 <= q_start[b] <= q_start[b+1] <= N. n_new must be NULL.
- * Rows that belong to no sequence have no effect and are never written. */
+ * Rows that belong to no sequence have no effect and are never written. Starts that are out of
+ * range or decrease make their own sequence DSPARK_SEQ_BAD_PARAM and leave the others as they
+ * would be without it; rows that two sequences then share hold the result of either. */
 typedef struct {
   int B, N;
   const int32_t* n_new;   /* device [B] or NULL */
@@ -111,7 +113,9 @@ dspark_status_t dspark_rotary_frequencies(int R, double theta, dspark_rotary_sca
  *  float32, rounded once to `dtype` (DSPARK_BF16 or DSPARK_F16).
  *  inv_freq  device float [R/2], R even in [0, head_dim], head_dim <= 1024 (R == 0: no rotation,
  *            inv_freq may be NULL).
- *  A sequence needs kv_len[b] >= n (else DSPARK_SEQ_BAD_PARAM). A token whose page id is out
+ *  A sequence needs kv_len[b] >= n (else DSPARK_SEQ_BAD_PARAM). A packed row that two sequences
+ *  claim (where starts decrease) is appended for one of them; a sequence that may lack such a
+ *  row is DSPARK_SEQ_BAD_PARAM, though its other rows are appended. A token whose page id is out
  *  of range is not appended (DSPARK_SEQ_BAD_PAGE); its query is rotated as usual.
  *  status    device [B] or NULL: 0 or DSPARK_SEQ_* bits.
  *  No workspace. Slots must not be shared by two new tokens (their order is not defined). */

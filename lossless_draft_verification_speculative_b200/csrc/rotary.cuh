@@ -102,31 +102,67 @@ struct RotaryToken {
   int64_t k_at, v_at;  // the slot's element offset in the cache, or -1
 };
 
+// The largest b in [0, B) with q_start[b] <= row, or -1, found by a warp: 32 starts a step, one
+// load and ballot per factor of 32 in B. Where the starts decrease somewhere, some index.
+__device__ __forceinline__ int packed_search(const dspark_rows_t& r, int row, int lane) {
+  int lo = -1, hi = r.B;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + (lane + 1) * step;
+    const bool le = at < hi && r.q_start[at] <= row;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, le));
+    const int nlo = lo + cnt * step;
+    hi = min(hi, nlo + step);
+    lo = nlo;
+  }
+  return lo;
+}
+
+// Whether sequence b, by its own bounds, has some of the rows first .. last.
+__device__ __forceinline__ bool packed_claims(const dspark_rows_t& r, int b, int first, int last) {
+  const int s0 = r.q_start[b], s1 = r.q_start[b + 1];
+  return 0 <= s0 && s0 <= last && first < s1 && s0 < s1 && s1 <= r.N;
+}
+
+// The first sequence that claims a row, or -1. (For rows whose search was misled by starts that
+// decrease, and for rows of no sequence: a warp over all starts.)
+__device__ __forceinline__ int packed_scan(const dspark_rows_t& r, int row, int lane) {
+  int b = r.B;
+#pragma unroll 4
+  for (int at = lane; at < r.B; at += 32)
+    if (packed_claims(r, at, row, row)) b = min(b, at);
+  b = __reduce_min_sync(0xffffffffu, b);
+  return b < r.B ? b : -1;
+}
+
+// Whether every row of sequence b (packed, well-formed bounds, at least one row) is taken as its
+// own: the searches for its first and its last row both end at b (a larger row never ends lower,
+// so those between do too), or, where starts decrease, no other sequence claims one of its rows.
+__device__ __forceinline__ bool packed_sole(const dspark_rows_t& r, int b, const SeqRows& s,
+                                            int lane) {
+  const int last = s.first + s.n - 1;
+  if (packed_search(r, s.first, lane) == b && packed_search(r, last, lane) == b) return true;
+  bool shared = false;
+  for (int at = lane; at < r.B; at += 32)
+    shared |= at != b && packed_claims(r, at, s.first, last);
+  return !__any_sync(0xffffffffu, shared);
+}
+
 // Which sequence a row belongs to, its position and its slot, found by one warp: block rows by
-// division, packed rows by a 32-way search of the non-decreasing q_start (one load and ballot
-// per factor of 32 in B). Ill-formed starts give some sequence or none, and seq_rows refuses
-// those out of range, so nothing is read outside the arrays.
+// division, packed rows by packed_search. A search that ends at a sequence without the row was
+// misled by another sequence's starts, or the row belongs to none: packed_scan tells. Bounds
+// out of range are refused by packed_claims and seq_rows, so nothing outside the arrays is read.
 __device__ __forceinline__ RotaryToken rotary_token(const RotaryParams& p, int row, int lane) {
   RotaryToken t{row, -1, -1, -1};
   const dspark_kv_cache_t& c = p.cache;
   int b;
   if (p.rows.q_start) {
-    // the largest b in [0, B) with q_start[b] <= row, or -1
-    int lo = -1, hi = p.rows.B;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int at = lo + (lane + 1) * step;
-      const bool le = at < hi && p.rows.q_start[at] <= row;
-      const int cnt = __popc(__ballot_sync(0xffffffffu, le));
-      const int nlo = lo + cnt * step;
-      hi = min(hi, nlo + step);
-      lo = nlo;
-    }
-    b = lo;
+    b = packed_search(p.rows, row, lane);
+    if (b < 0 || !packed_claims(p.rows, b, row, row)) b = packed_scan(p.rows, row, lane);
+    if (b < 0) return t;
   } else {
     b = row / p.rows.N;
   }
-  if (b < 0) return t;
   SeqRows s;
   const int64_t cap = static_cast<int64_t>(c.max_pages) * c.page_size;
   if (!seq_rows(p.rows, c.kv_len, cap, b, s) || s.L < s.n) return t;
@@ -177,6 +213,7 @@ __device__ __forceinline__ void rotary_status(const RotaryParams& p) {
         bad |= page < 0 || page >= c.n_pages;
       }
       if (__any_sync(0xffffffffu, bad)) st = DSPARK_SEQ_BAD_PAGE;
+      if (p.rows.q_start && !packed_sole(p.rows, b, s, lane)) st |= DSPARK_SEQ_BAD_PARAM;
     }
     if (lane == 0) p.status[b] = st;
   }
