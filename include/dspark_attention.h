@@ -137,7 +137,9 @@ dspark_status_t dspark_rotary_append(dspark_heads_t q, int n_q_heads, dspark_hea
  *  lse       device float [rows, n_q_heads] (block: [B, N, heads], packed: [N, heads]) or NULL:
  *            log of the sum of exp(scale * q . k_t) over the seen t (natural logarithm).
  *  status    device [B] or NULL. A token that sees a position whose page id is out of range
- *            gives NaN (DSPARK_SEQ_BAD_PAGE); the others are not affected.
+ *            gives NaN (DSPARK_SEQ_BAD_PAGE); the others are not affected. When the kernel gives up
+ *            on one of its (bounded) waits every sequence has DSPARK_SEQ_TIMEOUT: rows may be
+ *            unwritten or NaN, and dspark_pipeline_timeouts grows.
  *  Limits (else DSPARK_ERR_UNSUPPORTED): head_dim a multiple of 8 in [16, 128]; page_size a
  *  power of two in [8, 1024]; at most 4096 heads and 65535 sequences; pointers and strides
  *  multiples of 16 bytes, the cache's strides below 2^40 bytes.
@@ -155,7 +157,8 @@ dspark_status_t dspark_block_attention(dspark_heads_t q, int n_q_heads, dspark_h
 
 /* For tests of the timeout path only: dspark_block_attention with each CTA's first copy of keys
  * withheld, so that the waits for it run out (about a second) and the kernel gives up: the call
- * returns DSPARK_OK, its outputs are incomplete and dspark_pipeline_timeouts grows. */
+ * returns DSPARK_OK, its outputs are incomplete, every sequence has DSPARK_SEQ_TIMEOUT and
+ * dspark_pipeline_timeouts grows. */
 dspark_status_t dspark_block_attention_withheld(dspark_heads_t q, int n_q_heads,
                                                 dspark_heads_t out, dspark_dtype_t dtype,
                                                 dspark_kv_cache_t cache, dspark_rows_t rows,

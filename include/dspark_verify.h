@@ -86,7 +86,8 @@ typedef enum { DSPARK_BF16 = 0, DSPARK_F32 = 1, DSPARK_F16 = 2 } dspark_dtype_t;
 #define DSPARK_SEQ_NONFINITE 2     /* a row with NaN / +inf, or with no finite value       */
 #define DSPARK_SEQ_ZERO_RESIDUAL 4 /* not an error: residual mass rounded to 0 after a
                                       rejection; the correction was drawn from p_j          */
-#define DSPARK_SEQ_TIMEOUT 8       /* reserved: the kernels have no waits that can give up  */
+#define DSPARK_SEQ_TIMEOUT 8       /* dspark_block_attention: a kernel gave up on a wait; the
+                                      verify kernels have no waits that can give up         */
 #define DSPARK_SEQ_BAD_PARAM 16    /* dspark_mixed_accept: a draft count outside [0, K], or a
                                       negative or non-finite temperature (or one so small that
                                       log2(e)/T overflows)                                    */

@@ -47,8 +47,10 @@
 // tile against 2048 of the tensor cores' own; a one-tile item costs 12 us beside its launch.
 //
 // Waits. Every mbarrier wait is bounded (2^31 clocks, about a second); one that runs out sets an
-// abort flag that ends every role's loop, is counted (dspark_pipeline_timeouts), lets the copies
-// and products in flight finish (again bounded) and frees the tensor memory.
+// abort flag that ends every role's loop, is counted (dspark_pipeline_timeouts) and noted for the
+// kernel that joins pieces, which reports it (DSPARK_SEQ_TIMEOUT) and gives NaN for the items that
+// lack a piece; the CTA lets the copies and products in flight finish (again bounded) and frees the
+// tensor memory.
 //
 // Unseen places. Scores outside a row's range become -inf whatever they are. A weight of 0 times
 // a non-finite value would be NaN, so in a tile that some row of the item does not see in full
@@ -100,9 +102,10 @@ struct AttnParams {
 };
 
 // An item cut by a border: its first piece is in slot 2 cta + 1 of the CTA it begins in, the
-// others in slots 2 (cta + 1), 2 (cta + 2), ...; pieces == 0: nothing to join.
+// others in slots 2 (cta + 1), 2 (cta + 2), ...; pieces == 0: nothing to join. Every CTA writes its
+// record at its start, and at its end whether it gave up on a wait.
 struct AttnJoin {
-  int b, h, row0, rows, first, pieces;
+  int h, row0, rows, first, pieces, gave_up;
 };
 
 // What a CTA does with one item (or its piece of it).
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         off = u0 - __shfl_sync(0xffffffffu, upto - mine, at);
         b = at * per - 1;  // (the walk steps to the next sequence first)
       }
-      if (lane == 0) p.join[blockIdx.x].pieces = 0;
+      if (lane == 0) p.join[blockIdx.x] = AttnJoin{};
     }
     // the next item of the run (rows == 0: the end)
     auto deal = [&](AttnItem& it) {
@@ -566,8 +569,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         fixes += it.partials_before(it.t0 + it.nt);
         if (lane == 0 && t_lo == 0 && t_hi < nt)
           p.join[blockIdx.x] =
-              AttnJoin{b, h, row0, rows, sq.first,
-                       1 + static_cast<int>(quick_div(nt - t_hi + quota - 1, quota))};
+              AttnJoin{h, row0, rows, sq.first,
+                       1 + static_cast<int>(quick_div(nt - t_hi + quota - 1, quota)), 0};
         return;
       }
     };
@@ -1042,7 +1045,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *s_abort) atomicAdd(&g_pipeline_timeouts, 1ull);
+  if (tid == 0) {
+    const int gave_up = *s_abort;
+    p.join[blockIdx.x].gave_up = gave_up;
+    if (gave_up) atomicAdd(&g_pipeline_timeouts, 1ull);
+  }
   if (wi == 9) tmem_free_all(*s_tmem);
 }
 
@@ -1060,11 +1067,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const dspark_kv_cache_t& c = p.cache;
   const int G = p.Hq / c.n_heads;
-  if (p.status) {
+  const int b0 = (blockIdx.y * gridDim.x + blockIdx.x) * kJoinWarps + warp;
+  if (p.status && b0 < p.rows.B) {
     const int warps = gridDim.x * gridDim.y * kJoinWarps;
     const int64_t cap = static_cast<int64_t>(c.max_pages) << p.page_log2;
-    for (int b = (blockIdx.y * gridDim.x + blockIdx.x) * kJoinWarps + warp; b < p.rows.B;
-         b += warps) {
+    int gave_up = 0;  // a CTA that gave up leaves any sequence's rows incomplete
+#pragma unroll 4
+    for (int x = lane; x < gridDim.x; x += 32) gave_up |= p.join[x].gave_up;
+    gave_up = __any_sync(0xffffffffu, gave_up) ? DSPARK_SEQ_TIMEOUT : 0;
+    for (int b = b0; b < p.rows.B; b += warps) {
       SeqRows s;
       const bool ok = seq_rows(p.rows, c.kv_len, cap, b, s);
       bool bad = false;
@@ -1079,7 +1090,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
           }
       }
       bad = __any_sync(0xffffffffu, bad);
-      if (lane == 0) p.status[b] = !ok ? DSPARK_SEQ_BAD_PARAM : bad ? DSPARK_SEQ_BAD_PAGE : 0;
+      if (lane == 0)
+        p.status[b] = gave_up | (!ok ? DSPARK_SEQ_BAD_PARAM : bad ? DSPARK_SEQ_BAD_PAGE : 0);
     }
   }
   const AttnJoin jn = p.join[blockIdx.x];
@@ -1087,9 +1099,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
   const int x = blockIdx.x;
   for (int r = blockIdx.y * kJoinWarps + warp; r < jn.rows; r += gridDim.y * kJoinWarps) {
     float m = -INFINITY;
+    int gave_up = 0;
     for (int i = lane; i < jn.pieces; i += 32) {
       const int slot = i == 0 ? 2 * x + 1 : 2 * (x + i);
       m = fmaxf(m, p.part_ml[static_cast<int64_t>(slot) * p.part_rows + r].x);
+      gave_up |= p.join[x + i].gave_up;
     }
     m = warp_max_nan(m);
     const float mu = m == -INFINITY ? 0.f : m;
@@ -1106,6 +1120,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
 #pragma unroll
       for (int k = 0; k < kPer; ++k) o[k] += p.part_o[pr * DP + lane * kPer + k] * a;
     }
+    if (__any_sync(0xffffffffu, gave_up)) l = NAN;  // a piece is missing
     const int token = (jn.row0 + r) / G, g = jn.row0 + r - token * G, row = jn.first + token;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     T* out = static_cast<T*>(p.out.p) + row_offset(p.out, p.rows, row) +
