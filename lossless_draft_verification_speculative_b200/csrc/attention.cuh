@@ -78,7 +78,16 @@ constexpr int kAtDescs = 4;         // items announced ahead
 constexpr int kAtBadRing = 16;      // tiles whose bad-page masks are kept
 constexpr int kAtFixRing = 8;       // tiles whose masks of zeroed values are kept
 constexpr float kAtRescale = 8.f;   // binary orders a new maximum may exceed the kept one
+// |c m| from which scores are reduced to z - m before the product with c: below it the rounding of
+// c m is at most 2^-17, relative to a weight a 64th of f16's half step. (Always reducing them: 683
+// us instead of 623 for a 4096-token chunk at 12288; the instructions lie on a warp's chain.)
+constexpr float kAtLargeScore = 128.f;
 
+// Binary orders by which the weights (and l and O) are enlarged.
+template <typename T>
+__host__ __device__ constexpr float at_shift() {
+  return std::is_same<T, __half>::value ? 7.f : 0.f;
+}
 __host__ __device__ constexpr int at_stage_bytes(int dp) { return kAtTile * dp * 2; }
 __host__ __device__ constexpr int at_stages(int dp) { return dp == 128 ? 5 : 10; }
 
@@ -97,7 +106,7 @@ struct AttnParams {
   int which_k, which_v;  // last coordinate of keys and of values in their tensor maps
   int withhold;      // (tests of the timeout path) each CTA's first K copy is not issued
   float* part_o;     // [2 CTAs][part_rows][DP]
-  float2* part_ml;   // [2 CTAs][part_rows]: (c m, less the weights' enlargement; l)
+  float2* part_ml;   // [2 CTAs][part_rows]: (m; l)
   struct AttnJoin* join;  // [CTAs]
 };
 
@@ -350,7 +359,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                      const __grid_constant__ AttnParams p) {
   using Sm = AttnSmem<DP>;
   constexpr bool kBf = sizeof(T) == 2 && !std::is_same<T, __half>::value;
-  constexpr float kShift = kBf ? 0.f : 7.f;  // binary orders by which the weights are enlarged
+  constexpr float kShift = at_shift<T>();
   constexpr int kStages = Sm::kStages;
   constexpr int kHalves = DP / 64;
   extern __shared__ __align__(1024) uint8_t at_smem[];
@@ -891,7 +900,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           if (real) {
             if (it.slot >= 0)
-              p.part_ml[pr] = make_float2(m == -INFINITY ? m : m * cl - kShift, l);
+              p.part_ml[pr] = make_float2(m, l);
             else if (p.lse)
               p.lse[static_cast<int64_t>(row) * p.Hq + head] =
                   l == 0.f ? -INFINITY : (m * cl - kShift + log2f(l)) * 0.69314718055994531f;
@@ -925,7 +934,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       seen_range(it.L, it.n, token, p.causal, p.window, lo, hi);
       m = -INFINITY;
       l = 0.f;
-      bool poison = false;
+      bool poison = false, large = false;
 
       for (int k = 0; k < cnt && live; ++k) {
         const int j = dual ? k : 2 * k + rel;
@@ -969,6 +978,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const float f = move ? ex2((m - mn) * cl) : 1.f;  // m == -inf: 0
             l *= f;
             m = mn;
+            large = __any_sync(0xffffffffu, real && m != -INFINITY &&
+                                                fabsf(m) * cl > kAtLargeScore);
             if (k > 0) {
 #pragma unroll 1
               for (int q = 0; q < DP; q += 32) {
@@ -982,8 +993,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               }
             }
           }
-          // p = 2^(c z - c m), two at a time; 0 in rows past the item's
-          const float base = !real ? -INFINITY : m == -INFINITY ? 0.f : kShift - m * cl;
+          // p = 2^(c z - c m), two at a time; 0 in rows past the item's. The rounding of c m puts
+          // all of a row's weights off by half a place of c m (for scores of 10^8, by up to four
+          // binary orders), so large scores are reduced to z - m first.
+          const bool seen_any = m != -INFINITY;
+          if (large) {
+            const float minus_m = seen_any ? -m : 0.f;
+            const uint64_t m2 = pk2(minus_m, minus_m);
+#pragma unroll
+            for (int q = 0; q < kAtTile; q += 2)
+              upk2(add2(pk2(z[q], z[q + 1]), m2), z[q], z[q + 1]);
+          }
+          const float base = !real ? -INFINITY : large || !seen_any ? kShift : kShift - m * cl;
           const float factor = real ? cl : 0.f;
           const uint64_t c2 = pk2(factor, factor), base2 = pk2(base, base);
           uint64_t sum[4] = {0, 0, 0, 0};
@@ -1056,12 +1077,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 // ------------------------------------------------------------------------ joining pieces
 
 // The items that a border cut, and the sequences' status. CTA (x, y): item of CTA x of the
-// attention kernel, a warp per row. With m_i (scaled to base 2), l_i and O_i of the pieces and
-// M = max m_i: out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// attention kernel, a warp per row. With m_i, l_i and O_i of the pieces and M = max m_i:
+// out = sum 2^(c (m_i - M)) O_i / sum 2^(c (m_i - M)) l_i.
 constexpr int kJoinWarps = 8;
 template <typename T, int DP>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const AttnParams p) {
   constexpr int kPer = DP / 32;
+  constexpr float kShift = at_shift<T>();
+  const float cl = p.scale_log2;
   grid_dependency_wait();
   grid_dependents_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1115,7 +1138,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
       const int slot = i == 0 ? 2 * x + 1 : 2 * (x + i);
       const int64_t pr = static_cast<int64_t>(slot) * p.part_rows + r;
       const float2 ml = p.part_ml[pr];
-      const float a = ex2(ml.x - mu);  // -inf: 0
+      const float a = ex2((ml.x - mu) * cl);  // -inf: 0
       l += ml.y * a;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) o[k] += p.part_o[pr * DP + lane * kPer + k] * a;
@@ -1135,7 +1158,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
     }
     if (p.lse && lane == 0)
       p.lse[static_cast<int64_t>(row) * p.Hq + jn.h * G + g] =
-          l == 0.f ? -INFINITY : (mu + log2f(l)) * 0.69314718055994531f;
+          l == 0.f ? -INFINITY : (mu * cl - kShift + log2f(l)) * 0.69314718055994531f;
   }
 }
 
