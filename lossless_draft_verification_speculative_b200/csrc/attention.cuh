@@ -461,6 +461,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           s_bad[((it.load0 / 2 + j) % kAtBadRing) * 4 + lane] = m;
         }
+        __syncwarp();  // (lane 0's arrive below releases all four words)
         if (!wait(kBarEmpty + st, (g / kStages) ^ 1)) return false;
         if (p.withhold && g == 0 && is_k) continue;
         if (lane == 0)
