@@ -145,7 +145,8 @@ dspark_status_t dspark_rotary_append(dspark_heads_t q, int n_q_heads, dspark_hea
  *  multiples of 16 bytes, the cache's strides below 2^40 bytes.
  *  Numerics: scores and sums in float32 on the tensor cores; the weights are rounded to
  *  `dtype` for the product with v (a relative 2^-8 (bf16) or 2^-11 (f16) each at most), the
- *  statistics are not; out is rounded once.
+ *  statistics are not; out is rounded once, and finite values give a finite out (bf16: where
+ *  2^8 kv_len |v| stays below 2^127, as the weighted values are summed before the division).
  *  workspace  dspark_block_attention_workspace_bytes bytes, 256-byte aligned, no
  *            initialisation; one workspace serves one call at a time. */
 size_t dspark_block_attention_workspace_bytes(int N, int n_q_heads, int n_heads, int head_dim);

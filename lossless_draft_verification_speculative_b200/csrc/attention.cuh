@@ -258,6 +258,13 @@ __host__ __device__ constexpr uint32_t at_idesc(int n, bool bf, bool mn) {
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
+// A mean of finite f16 values lies within their range, but weights that were rounded up (by 2^-11)
+// can carry one next to the end over it, where f16 rounds to infinity. What is not finite stays.
+constexpr float kF16Max = 65504.f;
+__device__ __forceinline__ float f16_range(float x) {
+  return fabsf(x) < INFINITY ? fminf(fmaxf(x, -kF16Max), kF16Max) : x;
+}
+
 // ------------------------------------------------------------------------ units and items
 
 // Items of a (sequence, cache head) with R rows, and the tiles of an item.
@@ -887,13 +894,24 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
             } else {
 #pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] *= inv;
+              if (!kBf) {
+                float top = 0.f;
+#pragma unroll
+                for (int y = 0; y < 32; ++y) top = fmaxf(top, fabsf(o[y]));
+                if (top > kF16Max) {
+#pragma unroll
+                  for (int y = 0; y < 32; ++y) o[y] = f16_range(o[y]);
+                }
+              }
+#pragma unroll
               for (int y = 0; y < 32; y += 8) {
                 if (q + y < D) {
                   uint4 v;
-                  v.x = Half16<T>::down(o[y] * inv, o[y + 1] * inv);
-                  v.y = Half16<T>::down(o[y + 2] * inv, o[y + 3] * inv);
-                  v.z = Half16<T>::down(o[y + 4] * inv, o[y + 5] * inv);
-                  v.w = Half16<T>::down(o[y + 6] * inv, o[y + 7] * inv);
+                  v.x = Half16<T>::down(o[y], o[y + 1]);
+                  v.y = Half16<T>::down(o[y + 2], o[y + 3]);
+                  v.z = Half16<T>::down(o[y + 4], o[y + 5]);
+                  v.w = Half16<T>::down(o[y + 6], o[y + 7]);
                   *reinterpret_cast<uint4*>(out + q + y) = v;
                 }
               }
@@ -1149,13 +1167,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
     const float inv = l == 0.f ? 0.f : 1.f / l;
     T* out = static_cast<T*>(p.out.p) + row_offset(p.out, p.rows, row) +
              (jn.h * G + g) * p.out.head_stride;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      o[k] *= inv;
+      if (std::is_same<T, __half>::value) o[k] = f16_range(o[k]);
+    }
     if (lane * kPer < c.head_dim) {
       if (kPer == 4)
-        *reinterpret_cast<uint2*>(out + 4 * lane) =
-            make_uint2(Half16<T>::down(o[0] * inv, o[1] * inv),
-                       Half16<T>::down(o[kPer - 2] * inv, o[kPer - 1] * inv));
+        *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(
+            Half16<T>::down(o[0], o[1]), Half16<T>::down(o[kPer - 2], o[kPer - 1]));
       else
-        *reinterpret_cast<uint32_t*>(out + 2 * lane) = Half16<T>::down(o[0] * inv, o[1] * inv);
+        *reinterpret_cast<uint32_t*>(out + 2 * lane) = Half16<T>::down(o[0], o[1]);
     }
     if (p.lse && lane == 0)
       p.lse[static_cast<int64_t>(row) * p.Hq + jn.h * G + g] =

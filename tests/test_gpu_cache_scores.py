@@ -52,3 +52,38 @@ def test_scores_of_any_size(dtype, n, L, D, top):
     # round five times, by half of 2^-23 each of a value of this size
     assert (np.abs(z - want["lse"]) <= 6 * 2.0 ** -24 * np.abs(want["lse"])
             + 2.0 ** -20 + max(L) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("B,L", [(600, 300), (1, 128 * 600)])
+def test_f16_values_next_to_the_end_stay_finite(B, L):
+    """Values of 65504 everywhere: a weight just above a place's middle is rounded up by 2^-11, and
+    with it the mean, which f16 would make infinite from 65520 on. In every fourth tile, and in
+    the second after it, one key stands out, the latter by 7 binary orders and a little (below the
+    8 that move the kept maximum); whole items and joined ones."""
+    D = 16
+    c = Paged([L], 1, D, 128, "f16", seed=52)
+    c.v[c.v == c.v] = 65504.0
+    c.k[c.k == c.k] = 0.0
+    t = torch.arange(L)
+    page = c.table[0, t // 128].long()
+    c.k[page, t % 128, 0, 0] = -8.0
+    one, two = (t % 512 == 5), (t % 512 == 2 * 128 + 9)
+    c.k[page[one], t[one] % 128, 0, 0] = 0.0
+    c.k[page[two], t[two] % 128, 0, 0] = 1.0
+    d = c.device()
+    d.update(page_table=d["page_table"].repeat(B, 1),
+             kv_len=torch.full((B,), L, dtype=torch.int32, device=DEV))
+    q = torch.zeros(B, 1, 2, D, dtype=torch.float16, device=DEV)
+    q[..., 0] = 1.0
+    # 2^f for f between 0 and 2^-9 covers both sides of the middle between 1 and the next f16 value
+    for f in np.arange(0.0, 2.0 ** -9, 2.0 ** -14):
+        out = dv.block_attention(q, **d, scale=float((7 + f) * np.log(2.0)))
+        assert torch.isfinite(out).all(), f
+        # a weight's half step, and the result's
+        assert ((out.double() - 65504.0).abs() <= 65504.0 * 2.02 * 2.0 ** -11).all(), f
+    # an infinite value that a row sees still shows
+    c.v[page[5], 5, 0, 3] = float("inf")
+    d["v_pages"] = c.device()["v_pages"]
+    out = dv.block_attention(q, **d, scale=float(7 * np.log(2.0)))
+    torch.cuda.synchronize()
+    assert not torch.isfinite(out[..., 3]).any()
