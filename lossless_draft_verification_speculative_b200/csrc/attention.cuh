@@ -46,7 +46,8 @@
 // its burst rate). There a group's chain (scores, weights, both products) takes some 3600 clocks a
 // tile against 2048 of the tensor cores' own; a one-tile item costs 12 us beside its launch.
 //
-// Waits. Every mbarrier wait is bounded (2^31 clocks, about a second); one that runs out sets an
+// Waits. Every mbarrier wait is bounded (2^31 clocks, about a second; the zeroing warp's, which can
+// take as long as an item, 64 times that); one that runs out sets an
 // abort flag that ends every role's loop, is counted (dspark_pipeline_timeouts) and noted for the
 // kernel that joins pieces, which reports it (DSPARK_SEQ_TIMEOUT) and gives NaN for the items that
 // lack a piece; the CTA lets the copies and products in flight finish (again bounded) and frees the
@@ -227,13 +228,18 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, int 
 }
 
 // mbar_wait with little code (it is inlined often, and the kernel's code should stay in the
-// instruction cache): an expired wait sets the abort flag, which the CTA counts once at its end.
+// instruction cache): a wait that expires after kRounds times 2^31 clocks sets the abort flag,
+// which the CTA counts once at its end.
+template <int kRounds = 1>
 __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (mbar_try(bar, parity)) return true;
-  const uint32_t t0 = static_cast<uint32_t>(clock());
-  do {
-    if (mbar_try(bar, parity)) return true;
-  } while (!*abort && static_cast<uint32_t>(clock()) - t0 < (1u << 31));
+#pragma unroll 1
+  for (int k = 0; k < kRounds && !*abort; ++k) {
+    const uint32_t t0 = static_cast<uint32_t>(clock());
+    do {
+      if (mbar_try(bar, parity)) return true;
+    } while (!*abort && static_cast<uint32_t>(clock()) - t0 < (1u << 31));
+  }
   *abort = 1;
   return false;
 }
@@ -375,9 +381,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   auto bar = [&](int i) { return sb + Sm::kBars + 8 * i; };
   // a wait of the whole warp, with one outcome for all its lanes
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + Sm::kMisc + 4);
-  auto wait = [&](int i, uint32_t parity) {
-    return __all_sync(0xffffffffu, at_wait(bar(i), parity & 1, s_abort)) != 0;
+  auto wait_rounds = [&](auto rounds, int i, uint32_t parity) {
+    return __all_sync(0xffffffffu,
+                      at_wait<decltype(rounds)::value>(bar(i), parity & 1, s_abort)) != 0;
   };
+  constexpr std::integral_constant<int, 1> kOnce{};
+  auto wait = [&](int i, uint32_t parity) { return wait_rounds(kOnce, i, parity); };
   AttnItem* s_items = reinterpret_cast<AttnItem*>(sm + Sm::kItems);
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(sm + Sm::kBad);
   uint32_t* s_nf = reinterpret_cast<uint32_t*>(sm + Sm::kNf);
@@ -408,15 +417,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
   // the next announced item (rows == 0: the end); false on an abort
   int items = 0;
-  auto fetch = [&](AttnItem& to) {
+  auto fetch_rounds = [&](auto rounds, AttnItem& to) {
     const int d = items % kAtDescs;
-    if (!wait(kBarItem + d, items / kAtDescs)) return false;
+    if (!wait_rounds(rounds, kBarItem + d, items / kAtDescs)) return false;
     to = s_items[d];
     ++items;
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBarItemFree + d));
     return true;
   };
+  auto fetch = [&](AttnItem& to) { return fetch_rounds(kOnce, to); };
 
   if (wi >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
   if (wi == 8 || wi == 10) {
@@ -624,10 +634,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     // ------------------------------------------------------------------ unseen values
     // In a tile that some row of the item does not see in full: the values outside the item's
     // range become zeros, and so do those that only some rows see and that have an element that
-    // is not finite; the latter are noted.
+    // is not finite; the latter are noted. Such tiles are an item's first and last, so this warp
+    // waits while all the others pass: 2^23 tiles of some 4000 clocks at most (kv_len <= 2^30),
+    // 2^35 clocks. (A pipeline that stalls ends it sooner, through the other warps' flag.)
+    constexpr std::integral_constant<int, 64> kItemLong{};
     AttnItem it;
     bool live = true;
-    while (live && fetch(it) && it.rows > 0) {
+    while (live && fetch_rounds(kItemLong, it) && it.rows > 0) {
       const int look = look_ahead(it.rows, it.nt);
       const ItemRange rg = item_range(p, it.L, it.n, it.row0, it.rows);
       int fix = it.fix0;
@@ -636,7 +649,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const int g = it.load0 + load_of_v(j, look, it.nt);
         // (first that the copy was issued: before that the stage may still hold an earlier load,
         // whose phase a wait by parity could take for this one's)
-        live = wait(kBarToFix + fix % kAtFixRing, fix / kAtFixRing) &&
+        live = wait_rounds(kItemLong, kBarToFix + fix % kAtFixRing, fix / kAtFixRing) &&
                wait(kBarFull + g % kStages, g / kStages);
         if (!live) break;
 #pragma unroll 1
