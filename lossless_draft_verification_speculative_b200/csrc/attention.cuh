@@ -47,7 +47,7 @@
 // tile against 2048 of the tensor cores' own; a one-tile item costs 12 us beside its launch.
 //
 // Waits. Every mbarrier wait is bounded (2^31 clocks, about a second; the zeroing warp's, which can
-// take as long as an item, 64 times that); one that runs out sets an
+// take as long as an item, 32 times that); one that runs out sets an
 // abort flag that ends every role's loop, is counted (dspark_pipeline_timeouts) and noted for the
 // kernel that joins pieces, which reports it (DSPARK_SEQ_TIMEOUT) and gives NaN for the items that
 // lack a piece; the CTA lets the copies and products in flight finish (again bounded) and frees the
@@ -228,18 +228,20 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, int 
 }
 
 // mbar_wait with little code (it is inlined often, and the kernel's code should stay in the
-// instruction cache): a wait that expires after kRounds times 2^31 clocks sets the abort flag,
-// which the CTA counts once at its end.
+// instruction cache): a wait that expires (2^31 clocks, and 2^30 more for every further
+// round) sets the abort flag, which the CTA counts once at its end.
 template <int kRounds = 1>
 __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (mbar_try(bar, parity)) return true;
-#pragma unroll 1
-  for (int k = 0; k < kRounds && !*abort; ++k) {
-    const uint32_t t0 = static_cast<uint32_t>(clock());
-    do {
-      if (mbar_try(bar, parity)) return true;
-    } while (!*abort && static_cast<uint32_t>(clock()) - t0 < (1u << 31));
-  }
+  uint32_t t0 = static_cast<uint32_t>(clock());
+  int round = 1;
+  do {
+    if (mbar_try(bar, parity)) return true;
+    if (round < kRounds && static_cast<uint32_t>(clock()) - t0 >= (1u << 30)) {
+      t0 += 1u << 30;
+      ++round;
+    }
+  } while (!*abort && static_cast<uint32_t>(clock()) - t0 < (1u << 31));
   *abort = 1;
   return false;
 }
