@@ -46,6 +46,11 @@
 // its burst rate). There a group's chain (scores, weights, both products) takes some 3600 clocks a
 // tile against 2048 of the tensor cores' own; a one-tile item costs 12 us beside its launch.
 //
+// Sums. Tensor memory holds O of at most 64 tiles of a group (bf16: 256); then the group moves it
+// to a float32 sum in the workspace, by ordinary rounded additions. Without that equal weights over
+// 131072 positions gave values 4.6e-4 too small, over 524288 2.8e-3, and a sum of ones stopped at
+// 2^26.
+//
 // Waits. Every mbarrier wait is bounded (2^31 clocks, about a second; the zeroing warp's, which can
 // take as long as an item, 32 times that); one that runs out sets an
 // abort flag that ends every role's loop, is counted (dspark_pipeline_timeouts) and noted for the
@@ -89,6 +94,15 @@ template <typename T>
 __host__ __device__ constexpr float at_shift() {
   return std::is_same<T, __half>::value ? 7.f : 0.f;
 }
+// Tiles of a group after which its O moves from tensor memory to a sum in the workspace (a power of
+// two). The tensor cores cut each product off 25 places below the sum that it joins, a bias of up
+// to 128 x 2^-25 of O per tile: 2.4e-4 for 64 and 9.8e-4 for 256, half and a quarter of the half
+// step of f16 and bf16. (With 64 for bf16 too, a 4096-token chunk at 12288, where an item then
+// moves its sum once, took 665 us instead of 646.)
+template <typename T>
+__host__ __device__ constexpr int at_sum_tiles() {
+  return std::is_same<T, __half>::value ? 64 : 256;
+}
 __host__ __device__ constexpr int at_stage_bytes(int dp) { return kAtTile * dp * 2; }
 __host__ __device__ constexpr int at_stages(int dp) { return dp == 128 ? 5 : 10; }
 
@@ -109,6 +123,8 @@ struct AttnParams {
   float* part_o;     // [2 CTAs][part_rows][DP]
   float2* part_ml;   // [2 CTAs][part_rows]: (m; l)
   struct AttnJoin* join;  // [CTAs]
+  float* sums;       // [CTAs][2 groups][DP][sum_rows]: O of an item's earlier tiles (at_sum_tiles)
+  int sum_rows;
 };
 
 // An item cut by a border: its first piece is in slot 2 cta + 1 of the CTA it begins in, the
@@ -273,6 +289,39 @@ __device__ __forceinline__ float f16_range(float x) {
   return fabsf(x) < INFINITY ? fminf(fmaxf(x, -kF16Max), kF16Max) : x;
 }
 
+// O of a row (t_o: its warp's lanes and columns) plus f times the sum kept at `sum` (load), to
+// there (store) or back to tensor memory. Element d of the row is at sum[d * stride], so that a
+// warp's accesses are whole lines (16-byte accesses by row: 695 us for the chunk above with 64).
+// Not inlined: cold code between the hot costs instruction fetches.
+template <int DP>
+__device__ __noinline__ void at_move_sum(uint32_t t_o, float* sum, int stride, float f, bool load,
+                                         bool store, bool to_tmem) {
+#pragma unroll 1
+  for (int q = 0; q < DP; q += 32) {
+    float o[32];
+    tmem_ld32(t_o + q, o);
+    float a[32];
+#pragma unroll
+    for (int y = 0; y < 32; ++y) a[y] = load ? sum[(q + y) * stride] : 0.f;
+    __syncwarp();
+    tmem_ld_wait();
+#pragma unroll
+    for (int y = 0; y < 32; ++y) o[y] += a[y] * f;
+    if (store) {
+#pragma unroll
+      for (int y = 0; y < 32; ++y) sum[(q + y) * stride] = o[y];
+    }
+    __syncwarp();
+    if (to_tmem) {
+      uint32_t ow[32];
+#pragma unroll
+      for (int y = 0; y < 32; ++y) ow[y] = __float_as_uint(o[y]);
+      tmem_st32(t_o + q, ow);
+    }
+  }
+  if (to_tmem) tmem_st_wait();
+}
+
 // ------------------------------------------------------------------------ units and items
 
 // Items of a (sequence, cache head) with R rows, and the tiles of an item.
@@ -375,6 +424,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   using Sm = AttnSmem<DP>;
   constexpr bool kBf = sizeof(T) == 2 && !std::is_same<T, __half>::value;
   constexpr float kShift = at_shift<T>();
+  constexpr int kSumTiles = at_sum_tiles<T>();
   constexpr int kStages = Sm::kStages;
   constexpr int kHalves = DP / 64;
   extern __shared__ __align__(1024) uint8_t at_smem[];
@@ -764,7 +814,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             live = wait(kBarP + s, phase);
             if (!live) break;
             tc_fence_after();
-            pv(s, j, dual ? j == 0 : j < 2);
+            pv(s, j, (dual ? j : j >> 1) % kSumTiles == 0);
             if (x == 1) free_stage(load_of_v(j, look, nt));
             const int jn = j + (dual ? 1 : 2);
             if (jn < nt) {
@@ -842,7 +892,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     bool live = true, dual = false, active = false, real = false;
     int cnt = 0, row0 = 0, token = 0, head = 0;
     float m = -INFINITY, l = 0.f;
+    float m_sum = -INFINITY;  // the maximum that the sum of earlier tiles is relative to
     it.rows = 0;
+    // The row's O joins the sum of earlier tiles (first: there is none yet), which goes back to
+    // tensor memory (to_tmem) or to the workspace.
+    auto move_sum = [&](bool to_tmem, bool first) {
+      const float f = m_sum == -INFINITY ? 0.f : ex2((m_sum - m) * cl);
+      at_move_sum<DP>(t_o,
+                      p.sums + (2 * static_cast<int64_t>(blockIdx.x) + s) * DP * p.sum_rows + r,
+                      p.sum_rows, f, real && !first, real && !to_tmem, to_tmem);
+      m_sum = m;
+    };
     while (true) {
       live = fetch(next);
       if (!live) break;
@@ -854,6 +914,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           if (!live) break;
           ++n_o;
           tc_fence_after();
+          if (cnt > kSumTiles && active) {  // O of all tiles
+            move_sum(true, false);
+            tc_fence_before();
+          }
         }
         // both groups hold the same rows: the one of tile 0 takes the other's part in
         const bool pair = !dual && it.nt > 1;
@@ -966,129 +1030,139 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       head = it.h * G + mine_row - token * G;
       int lo, hi;
       seen_range(it.L, it.n, token, p.causal, p.window, lo, hi);
-      m = -INFINITY;
+      m = m_sum = -INFINITY;
       l = 0.f;
       bool poison = false, large = false;
 
-      for (int k = 0; k < cnt && live; ++k) {
-        const int j = dual ? k : 2 * k + rel;
-        const int x0 = (it.t0 + j) * kAtTile;
-        const bool partial = it.partial(it.t0 + j);
-        live = wait(kBarS + s, n_s);
-        if (!live) break;
-        ++n_s;
-        tc_fence_after();
-        if (active) {
-          float z[kAtTile];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, z + 32 * q);
-          tmem_ld_wait();
-          if (partial) {
-            // the row's seen positions as bits, 32 at a time
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int at = x0 + 32 * y;
-              const int a = min(max(lo - at, 0), 32), e = min(max(hi - at, 0), 32);
-              const uint32_t seen = static_cast<uint32_t>((1ull << e) - (1ull << min(a, e)));
-#pragma unroll
-              for (int q = 0; q < 32; ++q)
-                if (!((seen >> q) & 1)) z[32 * y + q] = -INFINITY;
-            }
-          }
-          float mx[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) mx[y] = max_nan(z[2 * y], z[2 * y + 1]);
-#pragma unroll
-          for (int q = 8; q < kAtTile; q += 8) {
-#pragma unroll
-            for (int y = 0; y < 4; ++y) mx[y] = max3_nan(mx[y], z[q + 2 * y], z[q + 2 * y + 1]);
-          }
-          const float mt = max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]);
-          if (!(mt < INFINITY)) poison = true;  // a NaN or an infinity among the seen scores
-          // the kept maximum moves when the tile's exceeds it by kAtRescale binary orders
-          const bool move = real && mt > m && !((mt - m) * cl <= kAtRescale);
-          if (__any_sync(0xffffffffu, move)) {
-            const float mn = move ? mt : m;
-            const float f = move ? ex2((m - mn) * cl) : 1.f;  // m == -inf: 0
-            l *= f;
-            m = mn;
-            large = __any_sync(0xffffffffu, real && m != -INFINITY &&
-                                                fabsf(m) * cl > kAtLargeScore);
-            if (k > 0) {
 #pragma unroll 1
-              for (int q = 0; q < DP; q += 32) {
-                float o[32];
-                tmem_ld32(t_o + q, o);
-                tmem_ld_wait();
-                uint32_t ow[32];
+      for (int k0 = 0; k0 < cnt && live; k0 += kSumTiles) {
+        if (k0 > 0) {  // (scores that are ready: the products before them are done)
+          live = wait(kBarS + s, n_s);
+          if (!live) break;
+          tc_fence_after();
+          if (active) move_sum(false, k0 == kSumTiles);
+        }
+        const int k1 = min(cnt, k0 + kSumTiles);
+        for (int k = k0; k < k1 && live; ++k) {
+          const int j = dual ? k : 2 * k + rel;
+          const int x0 = (it.t0 + j) * kAtTile;
+          const bool partial = it.partial(it.t0 + j);
+          live = wait(kBarS + s, n_s);
+          if (!live) break;
+          ++n_s;
+          tc_fence_after();
+          if (active) {
+            float z[kAtTile];
 #pragma unroll
-                for (int y = 0; y < 32; ++y) ow[y] = __float_as_uint(o[y] * f);
-                tmem_st32(t_o + q, ow);
+            for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, z + 32 * q);
+            tmem_ld_wait();
+            if (partial) {
+              // the row's seen positions as bits, 32 at a time
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int at = x0 + 32 * y;
+                const int a = min(max(lo - at, 0), 32), e = min(max(hi - at, 0), 32);
+                const uint32_t seen = static_cast<uint32_t>((1ull << e) - (1ull << min(a, e)));
+#pragma unroll
+                for (int q = 0; q < 32; ++q)
+                  if (!((seen >> q) & 1)) z[32 * y + q] = -INFINITY;
               }
             }
-          }
-          // p = 2^(c z - c m), two at a time; 0 in rows past the item's. The rounding of c m puts
-          // all of a row's weights off by half a place of c m (for scores of 10^8, by up to four
-          // binary orders), so large scores are reduced to z - m first.
-          const bool seen_any = m != -INFINITY;
-          if (large) {
-            const float minus_m = seen_any ? -m : 0.f;
-            const uint64_t m2 = pk2(minus_m, minus_m);
+            float mx[4];
 #pragma unroll
-            for (int q = 0; q < kAtTile; q += 2)
-              upk2(add2(pk2(z[q], z[q + 1]), m2), z[q], z[q + 1]);
-          }
-          const float base = !real ? -INFINITY : large || !seen_any ? kShift : kShift - m * cl;
-          const float factor = real ? cl : 0.f;
-          const uint64_t c2 = pk2(factor, factor), base2 = pk2(base, base);
-          uint64_t sum[4] = {0, 0, 0, 0};
+            for (int y = 0; y < 4; ++y) mx[y] = max_nan(z[2 * y], z[2 * y + 1]);
 #pragma unroll
-          for (int q = 0; q < kAtTile; q += 64) {
-            uint32_t pw[32];
+            for (int q = 8; q < kAtTile; q += 8) {
 #pragma unroll
-            for (int y = 0; y < 32; ++y) {
-              float e0, e1;
-              upk2(fma2(pk2(z[q + 2 * y], z[q + 2 * y + 1]), c2, base2), e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              sum[y & 3] = add2(sum[y & 3], pk2(e0, e1));
-              pw[y] = Half16<T>::down(e0, e1);
+              for (int y = 0; y < 4; ++y) mx[y] = max3_nan(mx[y], z[q + 2 * y], z[q + 2 * y + 1]);
             }
-            tmem_st32(t_s + q / 2, pw);
-          }
-          {
-            float s0, s1;
-            upk2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
-            l += s0 + s1;
-          }
-          tmem_st_wait();
-        }
-        if (owed) {  // before this group's O may be written again
-          live = wait(kBarJoined, owed_phase);
-          if (!live) break;
-          owed = false;
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + s));
-        // positions in a page out of range, or whose value was not finite and is now zero
-        uint4 hit = *reinterpret_cast<const uint4*>(
-            s_bad + ((it.load0 / 2 + j) % kAtBadRing) * 4);
-        if (partial) {
-          const int fix = it.fix0 + it.partials_before(it.t0 + j);
-          live = wait(kBarFix + fix % kAtFixRing, fix / kAtFixRing);
-          if (!live) break;
-          const uint4 nf = *reinterpret_cast<const uint4*>(s_nf + (fix % kAtFixRing) * 4);
-          hit.x |= nf.x;
-          hit.y |= nf.y;
-          hit.z |= nf.z;
-          hit.w |= nf.w;
-        }
-        if (hit.x | hit.y | hit.z | hit.w) {
+            const float mt = max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]);
+            if (!(mt < INFINITY)) poison = true;  // a NaN or an infinity among the seen scores
+            // the kept maximum moves when the tile's exceeds it by kAtRescale binary orders
+            const bool move = real && mt > m && !((mt - m) * cl <= kAtRescale);
+            if (__any_sync(0xffffffffu, move)) {
+              const float mn = move ? mt : m;
+              const float f = move ? ex2((m - mn) * cl) : 1.f;  // m == -inf: 0
+              l *= f;
+              m = mn;
+              large = __any_sync(0xffffffffu, real && m != -INFINITY &&
+                                                  fabsf(m) * cl > kAtLargeScore);
+              if (k > k0) {
 #pragma unroll 1
-          for (int q = max(lo - x0, 0); q < min(hi - x0, kAtTile); ++q) {
-            const uint32_t word = q < 64 ? (q < 32 ? hit.x : hit.y) : (q < 96 ? hit.z : hit.w);
-            if ((word >> (q & 31)) & 1) poison = true;
+                for (int q = 0; q < DP; q += 32) {
+                  float o[32];
+                  tmem_ld32(t_o + q, o);
+                  tmem_ld_wait();
+                  uint32_t ow[32];
+#pragma unroll
+                  for (int y = 0; y < 32; ++y) ow[y] = __float_as_uint(o[y] * f);
+                  tmem_st32(t_o + q, ow);
+                }
+              }
+            }
+            // p = 2^(c z - c m), two at a time; 0 in rows past the item's. The rounding of c m puts
+            // all of a row's weights off by half a place of c m (for scores of 10^8, by up to four
+            // binary orders), so large scores are reduced to z - m first.
+            const bool seen_any = m != -INFINITY;
+            if (large) {
+              const float minus_m = seen_any ? -m : 0.f;
+              const uint64_t m2 = pk2(minus_m, minus_m);
+#pragma unroll
+              for (int q = 0; q < kAtTile; q += 2)
+                upk2(add2(pk2(z[q], z[q + 1]), m2), z[q], z[q + 1]);
+            }
+            const float base = !real ? -INFINITY : large || !seen_any ? kShift : kShift - m * cl;
+            const float factor = real ? cl : 0.f;
+            const uint64_t c2 = pk2(factor, factor), base2 = pk2(base, base);
+            uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < kAtTile; q += 64) {
+              uint32_t pw[32];
+#pragma unroll
+              for (int y = 0; y < 32; ++y) {
+                float e0, e1;
+                upk2(fma2(pk2(z[q + 2 * y], z[q + 2 * y + 1]), c2, base2), e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                sum[y & 3] = add2(sum[y & 3], pk2(e0, e1));
+                pw[y] = Half16<T>::down(e0, e1);
+              }
+              tmem_st32(t_s + q / 2, pw);
+            }
+            {
+              float s0, s1;
+              upk2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+              l += s0 + s1;
+            }
+            tmem_st_wait();
+          }
+          if (owed) {  // before this group's O may be written again
+            live = wait(kBarJoined, owed_phase);
+            if (!live) break;
+            owed = false;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarP + s));
+          // positions in a page out of range, or whose value was not finite and is now zero
+          uint4 hit = *reinterpret_cast<const uint4*>(
+              s_bad + ((it.load0 / 2 + j) % kAtBadRing) * 4);
+          if (partial) {
+            const int fix = it.fix0 + it.partials_before(it.t0 + j);
+            live = wait(kBarFix + fix % kAtFixRing, fix / kAtFixRing);
+            if (!live) break;
+            const uint4 nf = *reinterpret_cast<const uint4*>(s_nf + (fix % kAtFixRing) * 4);
+            hit.x |= nf.x;
+            hit.y |= nf.y;
+            hit.z |= nf.z;
+            hit.w |= nf.w;
+          }
+          if (hit.x | hit.y | hit.z | hit.w) {
+#pragma unroll 1
+            for (int q = max(lo - x0, 0); q < min(hi - x0, kAtTile); ++q) {
+              const uint32_t word = q < 64 ? (q < 32 ? hit.x : hit.y) : (q < 96 ? hit.z : hit.w);
+              if ((word >> (q & 31)) & 1) poison = true;
+            }
           }
         }
       }

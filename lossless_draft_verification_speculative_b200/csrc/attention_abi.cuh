@@ -88,10 +88,11 @@ dspark_status_t rotary_launch(RotaryParams p, bool vec, cudaStream_t stream) {
 }
 
 // Workspace of block_attention: the cut items, then the partial results' (m, l) and O of two
-// slots per CTA, for as many rows as an item of the call can have.
+// slots per CTA, for as many rows as an item of the call can have, then the sums of long items of
+// two groups per CTA.
 struct AttnWs {
-  size_t join, ml, o, total;
-  int part_rows;
+  size_t join, ml, o, sums, total;
+  int part_rows, sum_rows;
 };
 AttnWs attention_ws(int N, int Hq, int Hk, int D) {
   const long long rows = static_cast<long long>(N) * (Hq / Hk);
@@ -100,7 +101,10 @@ AttnWs attention_ws(int N, int Hq, int Hk, int D) {
   const size_t slots = 2 * static_cast<size_t>(kPlanSMs) * w.part_rows;
   w.ml = align256(sizeof(AttnJoin) * kPlanSMs);
   w.o = w.ml + align256(slots * sizeof(float2));
-  w.total = w.o + align256(slots * (D <= 64 ? 64 : 128) * sizeof(float));
+  w.sums = w.o + align256(slots * (D <= 64 ? 64 : 128) * sizeof(float));
+  w.sum_rows = w.part_rows < kAtTile ? w.part_rows : kAtTile;
+  w.total = w.sums + 2 * static_cast<size_t>(kPlanSMs) * w.sum_rows *
+                         align256((D <= 64 ? 64 : 128) * sizeof(float));
   return w;
 }
 
@@ -231,6 +235,8 @@ dspark_status_t block_attention_impl(dspark_heads_t q, int n_q_heads, dspark_hea
   p.join = reinterpret_cast<AttnJoin*>(w + ws.join);
   p.part_ml = reinterpret_cast<float2*>(w + ws.ml);
   p.part_o = reinterpret_cast<float*>(w + ws.o);
+  p.sums = reinterpret_cast<float*>(w + ws.sums);
+  p.sum_rows = ws.sum_rows;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == DSPARK_BF16)
     return D <= 64 ? attention_launch<__nv_bfloat16, 64>(p, dtype, ws, s)
