@@ -143,10 +143,14 @@ dspark_status_t dspark_rotary_append(dspark_heads_t q, int n_q_heads, dspark_hea
  *  Limits (else DSPARK_ERR_UNSUPPORTED): head_dim a multiple of 8 in [16, 128]; page_size a
  *  power of two in [8, 1024]; at most 4096 heads and 65535 sequences; pointers and strides
  *  multiples of 16 bytes, the cache's strides below 2^40 bytes.
- *  Numerics: scores and sums in float32 on the tensor cores; the weights are rounded to
- *  `dtype` for the product with v (a relative 2^-8 (bf16) or 2^-11 (f16) each at most), the
- *  statistics are not; out is rounded once, and finite values give a finite out (bf16: where
- *  2^8 kv_len |v| stays below 2^127, as the weighted values are summed before the division).
+ *  Numerics: scores and sums in float32 (products on the tensor cores, their sums moved on
+ *  before the cut-off there adds up to a quarter or half of the type's half step); the weights
+ *  are rounded to `dtype` for the product with v, the statistics are not. A weight is off by a
+ *  relative 2^-8 (bf16), or by a relative 2^-11 and 2^-37 of the row's largest weight (f16: with
+ *  equal small weights beside one large, noticeable from some 2^26 positions on). out is rounded
+ *  once, and finite values give a finite out (bf16: where 2^8 kv_len |v| stays below 2^127, as
+ *  the weighted values are summed before the division). A row whose seen scores are all -inf
+ *  gives zeros and lse -inf, as one that sees nothing.
  *  workspace  dspark_block_attention_workspace_bytes bytes, 256-byte aligned, no
  *            initialisation; one workspace serves one call at a time. */
 size_t dspark_block_attention_workspace_bytes(int N, int n_q_heads, int n_heads, int head_dim);

@@ -7,9 +7,10 @@
 // p_t v_t to O (c = log2 e); when a new maximum exceeds m by more than 8 binary orders, l and O
 // are scaled by 2^(c m - c m'). Smaller excesses leave m as it is: p then reaches at most 2^8,
 // which costs float32 and the 16-bit weights no precision, and the rescaling of O is rare. f16
-// weights (and with them l and O) are made 2^7 times larger, up to 2^15: unscaled, the small
-// weights of a long context, each below 2^-25, would vanish while l counts them; now those below
-// 2^-32 do, 2^-12 of the result for 2^20 of them.
+// weights (and with them l and O) are made 2^12 times larger and may exceed that by 3 orders, up to
+// 2^15: unscaled, the small weights of a long context, each below 2^-25, would vanish while l
+// counts them. Now a weight is off by at most 2^-37 of the largest (f16's subnormal half step)
+// beside its relative 2^-11: 2^-17 of the result for 2^20 of them.
 //
 // What bounds it. The keys and values of a cache head are read once for all G query heads that
 // share it and all new tokens of the sequence: with few tokens 2 head_dim 2 bytes of HBM per
@@ -83,7 +84,6 @@ constexpr int kAtItemUnits = 3;     // what an item costs beside its tiles, in t
 constexpr int kAtDescs = 4;         // items announced ahead
 constexpr int kAtBadRing = 16;      // tiles whose bad-page masks are kept
 constexpr int kAtFixRing = 8;       // tiles whose masks of zeroed values are kept
-constexpr float kAtRescale = 8.f;   // binary orders a new maximum may exceed the kept one
 // |c m| from which scores are reduced to z - m before the product with c: below it the rounding of
 // c m is at most 2^-17, relative to a weight a 64th of f16's half step. (Always reducing them: 683
 // us instead of 623 for a 4096-token chunk at 12288; the instructions lie on a warp's chain.)
@@ -92,7 +92,12 @@ constexpr float kAtLargeScore = 128.f;
 // Binary orders by which the weights (and l and O) are enlarged.
 template <typename T>
 __host__ __device__ constexpr float at_shift() {
-  return std::is_same<T, __half>::value ? 7.f : 0.f;
+  return std::is_same<T, __half>::value ? 12.f : 0.f;
+}
+// Binary orders that a new maximum may exceed the kept one by.
+template <typename T>
+__host__ __device__ constexpr float at_rescale() {
+  return std::is_same<T, __half>::value ? 3.f : 8.f;
 }
 // Tiles of a group after which its O moves from tensor memory to a sum in the workspace (a power of
 // two). The tensor cores cut each product off 25 places below the sum that it joins, a bias of up
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                      const __grid_constant__ AttnParams p) {
   using Sm = AttnSmem<DP>;
   constexpr bool kBf = sizeof(T) == 2 && !std::is_same<T, __half>::value;
-  constexpr float kShift = at_shift<T>();
+  constexpr float kShift = at_shift<T>(), kRescale = at_rescale<T>();
   constexpr int kSumTiles = at_sum_tiles<T>();
   constexpr int kStages = Sm::kStages;
   constexpr int kHalves = DP / 64;
@@ -1078,8 +1083,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
             const float mt = max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]);
             if (!(mt < INFINITY)) poison = true;  // a NaN or an infinity among the seen scores
-            // the kept maximum moves when the tile's exceeds it by kAtRescale binary orders
-            const bool move = real && mt > m && !((mt - m) * cl <= kAtRescale);
+            // the kept maximum moves when the tile's exceeds it by kRescale binary orders
+            const bool move = real && mt > m && !((mt - m) * cl <= kRescale);
             if (__any_sync(0xffffffffu, move)) {
               const float mn = move ? mt : m;
               const float f = move ? ex2((m - mn) * cl) : 1.f;  // m == -inf: 0

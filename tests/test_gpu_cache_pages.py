@@ -9,7 +9,8 @@ from cache_helpers import DEV, Paged, queries
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("ps,L,window", [(16, 300, 40), (16, 300, None), (8, 257, 1), (64, 512, 130)])
+@pytest.mark.parametrize("ps,L,window", [(16, 300, 40), (16, 300, None), (8, 257, 1),
+                                         (64, 512, 130)])
 @pytest.mark.parametrize("D,Hq", [(64, 1), (128, 4)])
 def test_each_bad_page_reaches_the_tokens_that_see_it(ps, L, window, D, Hq):
     """One sequence per page, on the same pages but for that one, whose id is out of range."""

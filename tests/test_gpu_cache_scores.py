@@ -87,3 +87,87 @@ def test_f16_values_next_to_the_end_stay_finite(B, L):
     out = dv.block_attention(q, **d, scale=float(7 * np.log(2.0)))
     torch.cuda.synchronize()
     assert not torch.isfinite(out[..., 3]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("orders", [12.3, 20.7, 27.6, 29.4, 33.1])
+@pytest.mark.parametrize("first", [True, False])
+def test_small_weights_count(dtype, orders, first):
+    """One key stands out by many binary orders over 65535 equal ones, with values that make the
+    result consist of these alone. Each is off by half a step of its type, relative, and in f16 by
+    2^-37 of the largest weight; the sum of float32 products and the result's rounding come on top
+    (an f16 result may be subnormal: half of 2^-24)."""
+    L, D = 65536, 16
+    c = Paged([L], 1, D, 256, dtype, seed=43)
+    at = 5 if first else L - 40
+    page, slot = c.table[0, at // 256].item(), at % 256
+    c.k.zero_()
+    c.v.fill_(16384.0)
+    c.k[page, slot, 0, 0], c.v[page, slot] = 1.0, 0.0
+    q = torch.zeros(1, 2, D, dtype=DT[dtype])
+    q[:, :, 0] = 8.0
+    o, _, want = _attend(c, q, [1], float(np.float32(orders * np.log(2.0) / 8.0)), dtype)
+    u = HALF_STEP[dtype]
+    weight = u + (2.0 ** (orders - 37) if dtype == "f16" else 0.0) + L * 2.0 ** -24
+    assert (np.abs(o - want["out"]) <= (u + weight) * want["out"] * 1.01 + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("orders", [12.3, 20.7, 27.6, 29.4, 33.1])
+@pytest.mark.parametrize("at", [5, 40000])
+def test_small_weights_count_in_one_item(dtype, orders, at):
+    """The same where one group of warps meets all 65536 keys: 256 query heads of each of 148
+    sequences, one item per CTA, whose pieces have no maxima of their own."""
+    B, G, L, D = 148, 256, 65536, 16
+    c = Paged([L], 1, D, 256, dtype, seed=43)
+    page, slot = c.table[0, at // 256].item(), at % 256
+    c.k.zero_()
+    c.v.fill_(16384.0)
+    c.k[page, slot, 0, 0], c.v[page, slot] = 1.0, 0.0
+    d = c.device()
+    d.update(page_table=d["page_table"].repeat(B, 1),
+             kv_len=torch.full((B,), L, dtype=torch.int32, device=DEV))
+    q = torch.zeros(B, 1, G, D, dtype=DT[dtype], device=DEV)
+    q[..., 0] = 8.0
+    lse = torch.zeros(B, 1, G, device=DEV)
+    out = dv.block_attention(q, **d, lse=lse, scale=float(np.float32(orders * np.log(2.0) / 8.0)))
+    w = (L - 1) * 2.0 ** -orders
+    want = 16384.0 * w / (1 + w)
+    u = HALF_STEP[dtype]
+    weight = u + (2.0 ** (orders - 37) if dtype == "f16" else 0.0) + L * 2.0 ** -24
+    err = (out.double() - want).abs().max().item()
+    assert err <= (u + weight) * want * 1.01 + 2.0 ** -25
+    z = orders * np.log(2.0) + np.log1p(w)
+    assert (lse.double() - z).abs().max() <= 2.0 ** -20 * z + L * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_scores_of_minus_infinity(dtype):
+    """A seen score of -inf has a weight of 0; a row that has no other gives zeros and lse -inf."""
+    D, L, n = 64, 300, 3
+    c = Paged([L, L], 1, D, 16, dtype, seed=44)
+    g = torch.Generator().manual_seed(45)
+    q = torch.randn(2 * n, 2, D, generator=g).to(DT[dtype])
+    q[:, :, 0] = -1.0
+    q[:n, 1, 0] = 0.5
+    d = c.device()
+    k = d["k_pages"]
+    for b, which in ((0, range(0, L)), (1, range(0, L, 3))):
+        for t in which:
+            k[c.table[b, t // 16].item(), t % 16, 0, 0] = float("inf")
+    starts = torch.tensor([0, n, 2 * n], dtype=torch.int32, device=DEV)
+    lse = torch.zeros(2 * n, 2, device=DEV)
+    out = dv.block_attention(q.to(DEV), **d, q_start=starts, lse=lse)
+    torch.cuda.synchronize()
+    # sequence 0: every score -inf (head 0) or +inf (head 1)
+    assert (out[:n, 0] == 0).all() and torch.isneginf(lse[:n, 0]).all()
+    assert not torch.isfinite(out[:n, 1]).any()
+    # sequence 1: as if the keys with infinities were not there
+    keep = torch.tensor([t for t in range(L) if t % 3])
+    K, V = (torch.tensor(x)[:, 0] for x in c.rows(1))
+    u = HALF_STEP[dtype]
+    for i in range(n):
+        mine = keep[keep <= L - n + i]
+        w = torch.softmax(q[n + i].double() @ K[mine].T * D ** -0.5, -1)
+        err = (out[n + i].double().cpu() - w @ V[mine]).abs()
+        assert (err <= 1.02 * u * (w @ V[mine].abs() + (w @ V[mine]).abs()) + 2.0 ** -16).all(), i
