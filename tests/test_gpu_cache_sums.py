@@ -92,3 +92,33 @@ def test_a_sum_of_201326592_ones():
                              torch.tensor([L], dtype=torch.int32, device=DEV))
     torch.cuda.synchronize()
     assert (out[..., :8] == 1.0).all() and (out[..., 8:] == 2.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [4, 256])
+@pytest.mark.parametrize("tiles", [148 * 300, 148 * 700 + 77])
+def test_long_pieces_are_summed_and_joined(dtype, n, tiles):
+    """One cache head over millions of positions: every CTA has a piece of hundreds of tiles, whose
+    sums leave tensor memory before the pieces are joined; every page but two is of eight."""
+    ps, D = 128, 64
+    k, v, g = _pool(10, ps, 1, D, dtype, 3)
+    table = torch.arange(tiles, device=DEV) % 8
+    table[tiles // 3], table[-1] = 8, 9
+    k[8] *= 2
+    q = torch.randn(1, n, 1, D, generator=g, device=DEV).to(DT[dtype])
+    lse = torch.zeros(1, n, 1, device=DEV)
+    out = dv.block_attention(q, k, v, table.to(torch.int32)[None],
+                             torch.tensor([tiles * ps], dtype=torch.int32, device=DEV),
+                             causal=False, lse=lse)
+    times = torch.bincount(table, minlength=10).double().repeat_interleave(ps)
+    K, V = k.reshape(-1, D).double(), v.reshape(-1, D).double()
+    z = q[0, :, 0].double() @ K.T * D ** -0.5 + times.log()
+    want_lse = z.logsumexp(-1)
+    want = (z - want_lse[:, None]).exp() @ V
+    e = 2 * ((q[0, :, 0].double().abs() @ K.abs().T).amax(-1) * D ** -0.5 * (D + 4) * 2.0 ** -24
+             + 2.0 ** -21)
+    err = (out[0, :, 0].double() - want).abs() / want
+    assert (err <= (2 * HALF_STEP[dtype] + CUT[dtype] + e[:, None]) * 1.01).all()
+    per = tiles // 148 + 128 + 148  # additions: a piece's tiles, a tile's places, the pieces
+    assert ((lse[0, :, 0].double() - want_lse).abs() <=
+            e + per * 2.0 ** -24 + 2.0 ** -22 * want_lse.abs() + 2.0 ** -22).all()
