@@ -103,14 +103,17 @@ struct RotaryToken {
 };
 
 // The largest b in [0, B) with q_start[b] <= row, or -1, found by a warp: 32 starts a step, one
-// load and ballot per factor of 32 in B. Where the starts decrease somewhere, some index.
+// load and ballot per factor of 32 in B. Where the starts decrease somewhere, some index. Rows from
+// the last start on, commonly padding, give -1 after the first step.
 __device__ __forceinline__ int packed_search(const dspark_rows_t& r, int row, int lane) {
+  const int end = r.q_start[r.B];
   int lo = -1, hi = r.B;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
     const int at = lo + (lane + 1) * step;
     const bool le = at < hi && r.q_start[at] <= row;
     const int cnt = __popc(__ballot_sync(0xffffffffu, le));
+    if (row >= end) return -1;
     const int nlo = lo + cnt * step;
     hi = min(hi, nlo + step);
     lo = nlo;
@@ -127,8 +130,8 @@ __device__ __forceinline__ bool packed_claims(const dspark_rows_t& r, int b, int
 // The first sequence that claims a row, or -1: for rows whose search was misled by starts that
 // decrease, and for rows of no sequence (those of a padded batch). A warp over all starts, many
 // loads in flight; not inlined, so that they cost the kernel no registers. (64 sequences and 3896
-// rows of padding: 9.8 us against 9.3 without; 1024 and 3072: 14.7 against 11.8, 15.1 inlined with
-// 4 loads in flight, 15.6 as a scan that the rows of a CTA share.)
+// rows of padding: 9.5 us against 9.3 without; 1024 and 3072: 14.3 against 11.8, more by 0.5 us
+// inlined with 4 loads in flight, by 0.9 as a scan that the rows of a CTA share.)
 __device__ __noinline__ int packed_scan(const int32_t* q_start, int B, int N, int row, int lane) {
   int b = B;
 #pragma unroll 16
@@ -160,18 +163,16 @@ __device__ __forceinline__ bool packed_sole(const dspark_rows_t& r, int b, const
 __device__ __forceinline__ RotaryToken rotary_token(const RotaryParams& p, int row, int lane) {
   RotaryToken t{row, -1, -1, -1};
   const dspark_kv_cache_t& c = p.cache;
-  int b;
-  if (p.rows.q_start) {
-    b = packed_search(p.rows, row, lane);
-    if (b < 0 || !packed_claims(p.rows, b, row, row))
-      b = packed_scan(p.rows.q_start, p.rows.B, p.rows.N, row, lane);
-    if (b < 0) return t;
-  } else {
-    b = row / p.rows.N;
-  }
-  SeqRows s;
   const int64_t cap = static_cast<int64_t>(c.max_pages) * c.page_size;
-  if (!seq_rows(p.rows, c.kv_len, cap, b, s) || s.L < s.n) return t;
+  int b = p.rows.q_start ? packed_search(p.rows, row, lane) : row / p.rows.N;
+  SeqRows s{};
+  // (the length is loaded beside the bounds, before they are looked at)
+  bool ok = b >= 0 && seq_rows(p.rows, c.kv_len, cap, b, s);
+  if (p.rows.q_start && (b < 0 || !packed_claims(p.rows, b, row, row))) {
+    b = packed_scan(p.rows.q_start, p.rows.B, p.rows.N, row, lane);
+    ok = b >= 0 && seq_rows(p.rows, c.kv_len, cap, b, s);
+  }
+  if (!ok || s.L < s.n) return t;
   const int i = row - s.first;
   if (i < 0 || i >= s.n) return t;
   t.pos = s.L - s.n + i;
@@ -230,10 +231,10 @@ __device__ __forceinline__ void rotary_status(const RotaryParams& p) {
 // the two halves of eight (i, i + R/2) pairs, or two neighbouring vectors (interleaved pairs,
 // the copied rest, v). A thread keeps its slot and takes every (256 / slots)-th (token, head); its
 // first one is loaded before the lengths, pages and angles are known, so that both latencies
-// overlap. Memory bound: 10205 tokens of 32 + 8 + 8 heads of 128 (251 MB) take 48.5 us, 5.2 TB/s,
-// 80% of the measured copy rate. Several loads in flight a thread cost more in registers (resident
-// warps) than they bring: 2, 4 and 6 took 51.2, 54.4 and 70.6 us; 2 or 8 tokens a CTA 48.8 and
-// above 50 us.
+// overlap. Memory bound: 10205 tokens of 32 + 8 + 8 heads of 128 (251 MB) take 46.8 us, 5.4 TB/s,
+// 83% of the measured copy rate. Several loads in flight a thread cost more in registers (resident
+// warps) than they bring: where one took 48.5 us, 2, 4 and 6 took 51.2, 54.4 and 70.6; 2 or 8
+// tokens a CTA 48.8 and above 50.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const RotaryParams p) {
   extern __shared__ __align__(16) float2 s_cs[];
