@@ -266,8 +266,8 @@ dspark_status_t dspark_markov_matvec(const void* table, dspark_table_t type, int
 
 /* The number of waits inside the library's pipelined kernels (the tensor-core mat-vecs) that
  * ran out (about a second each), and of CTAs of block_attention that gave up on one, on the
- * current device since the library was loaded: 0 unless a kernel gave up; a kernel that gives up frees its resources and leaves its outputs
- * incomplete. Synchronous (waits for the device). DSPARK_ERR_INVALID_ARG for a NULL count. */
+ * current device since the library was loaded: 0 unless a kernel gave up; a kernel that gives up
+ * frees its resources and leaves its outputs incomplete. Synchronous (waits for the device). DSPARK_ERR_INVALID_ARG for a NULL count. */
 dspark_status_t dspark_pipeline_timeouts(unsigned long long* count);
 
 /* For tests of the timeout path only: dspark_markov_matvec with each CTA's first table copy

@@ -199,7 +199,8 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: to
     (int32 ``[B]``) counts the new tokens. ``inv_freq`` (float32, on the device) rotates the
     first ``2 len(inv_freq)`` elements of each head, as halves or as ``interleaved`` pairs; None
     rotates nothing. Returns the rotated queries (``out``, which may be ``q``). ``status`` (int32
-    ``[B]``) receives SEQ_BAD_PARAM / SEQ_BAD_PAGE bits.
+    ``[B]``) receives SEQ_BAD_PARAM / SEQ_BAD_PAGE bits. Any page_size, head_dim up to 1024 (what
+    ``block_attention`` reads has narrower limits).
     """
     lib = _lib()
     index, dtype, shape = q.get_device(), q.dtype, q.shape
@@ -247,9 +248,11 @@ def block_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     ``p = kv_len[b] - n + i`` and sees the positions below ``kv_len[b]`` that are ``<= p`` when
     ``causal`` (not: the whole block, as a block drafter does) and ``> p - window`` when a
     ``window`` is given. ``scale`` defaults to ``head_dim ** -0.5``. Returns ``out``, q's shape;
-    a token that sees nothing gives zeros. ``lse`` (float32, q's shape without head_dim)
-    receives the logarithm of each row's sum of exponentials, ``status`` (int32 ``[B]``) the
-    SEQ_* bits. ``workspace``: at least ``block_attention_workspace_bytes(N, ...)`` bytes; by
+    a token that sees nothing gives zeros. head_dim is a multiple of 8 in 16..128, page_size a
+    power of two in 8..1024. ``lse`` (float32, q's shape without head_dim) receives the logarithm
+    of each row's sum of exponentials, ``status`` (int32 ``[B]``) the SEQ_* bits: SEQ_BAD_PARAM,
+    SEQ_BAD_PAGE, and SEQ_TIMEOUT for all sequences of a call that gave up on a wait, whose
+    results are incomplete. ``workspace``: at least ``block_attention_workspace_bytes(N, ...)`` bytes; by
     default one is taken from PyTorch's allocator for each call.
     """
     lib = _lib()

@@ -41,10 +41,10 @@
 // Tensor memory: S_0, S_1 (128 columns each, P_s over S_s), O_0, O_1 (128 columns each).
 //
 // Measured (one B200, back to back in a graph): blocks of up to 8 tokens of 64 sequences over 1024
-// to 16384 positions, 32 / 8 heads of 128, 1.47 GB: 233 us, 6.3 TB/s, 98% of the measured copy
-// rate. A 4096-token chunk at 12288: 574 us, 1.2 PFLOP/s, 73% of cuBLAS's bf16 rate in a burst; 667
-// us in seconds-long loops, where the power limit sets the clock (cuBLAS itself then makes 86% of
-// its burst rate). There a group's chain (scores, weights, both products) takes some 3600 clocks a
+// to 16384 positions, 32 / 8 heads of 128, 1.47 GB: 232 us, 6.3 TB/s, 98% of the measured copy
+// rate; in seconds-long loops, where the power limit sets the clock, 248 us, 92%. A 4096-token chunk
+// at 12288: 589 us, 1.17 PFLOP/s, 71% of cuBLAS's bf16 rate in a burst; 671 us in such loops
+// (cuBLAS itself then makes 86% of its burst rate). There a group's chain (scores, weights, both products) takes some 3600 clocks a
 // tile against 2048 of the tensor cores' own; a one-tile item costs 12 us beside its launch.
 //
 // Sums. Tensor memory holds O of at most 64 tiles of a group (bf16: 256); then the group moves it

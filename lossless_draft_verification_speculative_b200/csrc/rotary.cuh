@@ -231,8 +231,8 @@ __device__ __forceinline__ void rotary_status(const RotaryParams& p) {
 // the two halves of eight (i, i + R/2) pairs, or two neighbouring vectors (interleaved pairs,
 // the copied rest, v). A thread keeps its slot and takes every (256 / slots)-th (token, head); its
 // first one is loaded before the lengths, pages and angles are known, so that both latencies
-// overlap. Memory bound: 10205 tokens of 32 + 8 + 8 heads of 128 (251 MB) take 46.8 us, 5.4 TB/s,
-// 83% of the measured copy rate. Several loads in flight a thread cost more in registers (resident
+// overlap. Memory bound: 10205 tokens of 32 + 8 + 8 heads of 128 (251 MB) take 47.6 us, 5.3 TB/s,
+// 82% of the measured copy rate. Several loads in flight a thread cost more in registers (resident
 // warps) than they bring: where one took 48.5 us, 2, 4 and 6 took 51.2, 54.4 and 70.6; 2 or 8
 // tokens a CTA 48.8 and above 50.
 template <typename T, bool kVec>
