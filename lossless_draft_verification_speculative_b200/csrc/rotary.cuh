@@ -129,9 +129,9 @@ __device__ __forceinline__ bool packed_claims(const dspark_rows_t& r, int b, int
 
 // The first sequence that claims a row, or -1: for rows whose search was misled by starts that
 // decrease, and for rows of no sequence (those of a padded batch). A warp over all starts, many
-// loads in flight; not inlined, so that they cost the kernel no registers. (64 sequences and 3896
-// rows of padding: 9.5 us against 9.3 without; 1024 and 3072: 14.3 against 11.8, more by 0.5 us
-// inlined with 4 loads in flight, by 0.9 as a scan that the rows of a CTA share.)
+// loads in flight; not inlined, so that they cost the kernel no registers. (4096 rows of which
+// 64 sequences have 200: 9.5 us against 9.3 without; 1024 sequences one each: 14.3 against 11.8,
+// more by 0.5 us inlined with 4 loads in flight, by 0.9 as a scan that the rows of a CTA share.)
 __device__ __noinline__ int packed_scan(const int32_t* q_start, int B, int N, int row, int lane) {
   int b = B;
 #pragma unroll 16
